@@ -31,6 +31,12 @@ SIGNATURES = {
                           _Z, _P]),
     "gdn_vda_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I, _I]),
     "gdn_readout_gate": (_I, [_P, _I, _P, _I, _P, ctypes.c_float, _P, _I, _I, _I, _I, _I, _P]),
+    "gdn_short_conv": (_I, [_P, _Z, _Z, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
+    "gdn_rotary": (_I, [_P, _Z, _Z, _Z, _P, _Z, _Z, _Z, _I, _P, _Z, _Z, _Z, _P, _Z, _Z, _Z, _I, _P, _I, _I, _P,
+                        ctypes.c_float, _I, _I, _I, _I, _I, _I, _P]),
+    "gdn_ssm_scan": (_I, [_P, _Z, _Z, _P, _Z, _Z, _P, _Z, _Z, _P, _Z, _Z, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I,
+                          _I, _I, _I, _I, _I, _P, _Z, _P]),
+    "gdn_ssm_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I, _I]),
     "gdn_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I, _I, _I]),
     "gdn_status_string": (ctypes.c_char_p, [_I]),
     "gdn_version": (ctypes.c_char_p, []),
@@ -139,6 +145,31 @@ def gdn_vda_workspace_size(B, F, U, H, dk, dv, bidir):
 
 def gdn_readout_gate(o, o_dt, z, z_dt, gamma, eps, y, y_dt, B, T, H, dv, stream):
     return load().gdn_readout_gate(o, o_dt, z, z_dt, gamma, eps, y, y_dt, B, T, H, dv, stream)
+
+
+def gdn_short_conv(x, x_batch_stride, x_token_stride, w, bias, state_in, state_out, y, lengths, B, T, C, K, silu, dt,
+                   stream):
+    return load().gdn_short_conv(x, x_batch_stride, x_token_stride, w, bias, state_in, state_out, y, lengths, B, T, C,
+                                 K, silu, dt, stream)
+
+
+def gdn_rotary(q, q_strides, q_out, q_out_strides, Hq, k, k_strides, k_out, k_out_strides, Hk, pos, pos_bits, axes,
+               freqs, scale, B, T, d, rot, interleaved, dt, stream):
+    """Strides: (batch, token, head) in elements."""
+    return load().gdn_rotary(q, *q_strides, q_out, *q_out_strides, Hq, k, *k_strides, k_out, *k_out_strides, Hk, pos,
+                             pos_bits, axes, freqs, scale, B, T, d, rot, interleaved, dt, stream)
+
+
+def gdn_ssm_scan(q, q_strides, k, k_strides, v, v_strides, dt, dt_strides, A, D, dt_bias, state_in, state_out, o,
+                 lengths, B, T, H, G, dk, dv, softplus, t, dt_t, workspace, ws_bytes, stream):
+    """Strides: (batch, token) in elements."""
+    return load().gdn_ssm_scan(q, *q_strides, k, *k_strides, v, *v_strides, dt, *dt_strides, A, D, dt_bias, state_in,
+                               state_out, o, lengths, B, T, H, G, dk, dv, softplus, t, dt_t, workspace, ws_bytes,
+                               stream)
+
+
+def gdn_ssm_workspace_size(B, T, H, G, dk, dv, t):
+    return int(load().gdn_ssm_workspace_size(B, T, H, G, dk, dv, t))
 
 
 def gdn_set_kernel_timing(on):

@@ -6,9 +6,14 @@ current torch stream.  No arithmetic of the scan happens here.
 """
 from __future__ import annotations
 
+import math
+from fractions import Fraction
+
 import torch
 
 from . import _lib
+
+_TWO_PI = 2 * Fraction("3.14159265358979323846264338327950288419716939937510")
 
 _DT = {torch.float32: _lib.GDN_F32, torch.bfloat16: _lib.GDN_BF16}
 
@@ -199,3 +204,268 @@ def vda_scan(q, k, v, alpha_frame, beta, U, *, bidir=False, state=None, state_bw
                            int(bool(bidir)), _DT[q.dtype], odt, _ptr(ws), nbytes, stream)
     _raise("gdn_vda_scan", st)
     return (o, s_out, s_out_b) if return_states else o
+
+
+# ---------------------------------------------------------------------------
+# Operators around the scan: inputs may be views (last dimension contiguous)
+# ---------------------------------------------------------------------------
+def _view(t, name, dtype=None, shape=None, device=None):
+    """A CUDA tensor whose last dimension is contiguous."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor (the library has no CPU path)" % name)
+    if device is not None and t.device != device:
+        raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("%s must be contiguous in its last dimension" % name)
+
+
+def _dense(t, name, dtype, shape, device):
+    _view(t, name, dtype, shape, device)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def _strides(t, n):
+    """Strides of the first n dimensions in elements; a dimension of one entry
+    has no stride of its own (torch may report any): its row's width."""
+    w = 1
+    for s in t.shape[n:]:
+        w *= s
+    return tuple(t.stride(i) if t.shape[i] > 1 else w for i in range(n))
+
+
+def _rows(t, name):
+    """The heads of a token are contiguous: [B, T, H, d] with any batch and token stride."""
+    if t.shape[2] > 1 and t.stride(2) != t.shape[3]:
+        raise ValueError("%s must have the heads of a token contiguous" % name)
+
+
+def _lengths(lengths, B, device):
+    if lengths is not None:
+        _dense(lengths, "lengths", torch.int32, (B,), device)
+
+
+def _run(name, device, fn, *args):
+    """Call fn(*args, stream) with `device` current, on its current stream."""
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    _raise(name, st)
+
+
+def _result(out, shape, dtype, device, lengths):
+    """The output: `out`, or a new tensor, zero behind the sequences of a padded batch."""
+    if out is None:
+        make = torch.empty if lengths is None else torch.zeros
+        return make(shape, dtype=dtype, device=device)
+    _dense(out, "out", dtype, shape, device)
+    return out
+
+
+def short_conv(x, w, bias=None, state=None, *, silu=True, lengths=None, return_state=True, out=None,
+               state_out=None):
+    """Short causal convolution over time, one filter per channel:
+    y[b,t,c] = act(bias[c] + sum_j w[c,j] x[b,t-(K-1)+j,c]), act = silu or none.
+
+    x: [B,T,C] (fp32 or bf16, any batch and token stride); w: [C,K] fp32, K in
+    2..4; bias: [C] fp32 or None; state: [B,K-1,C] of x's dtype, the inputs
+    before token 0, oldest first (None = zero); lengths: [B] int32, tokens of
+    each sequence of a padded batch.  Returns (y, last K-1 inputs) (the state
+    None if not asked).  A new y is zero behind a sequence's end, a given
+    `out` keeps what it held there."""
+    if x.dtype not in _DT:
+        raise ValueError("x must be float32 or bfloat16")
+    if x.dim() != 3 or w.dim() != 2:
+        raise ValueError("x must be [B, T, C] and w [C, K]")
+    B, T, C = x.shape
+    K = w.shape[1]
+    dev = x.device
+    _view(x, "x")
+    _dense(w, "w", torch.float32, (C, K), dev)
+    if not 2 <= K <= 4:
+        raise ValueError("w must have 2 to 4 taps, got %d" % K)
+    if bias is not None:
+        _dense(bias, "bias", torch.float32, (C,), dev)
+    if state is not None:
+        _dense(state, "state", x.dtype, (B, K - 1, C), dev)
+    _lengths(lengths, B, dev)
+    y = _result(out, (B, T, C), x.dtype, dev, lengths)
+    if state_out is not None:
+        _dense(state_out, "state_out", x.dtype, (B, K - 1, C), dev)
+    elif return_state:
+        state_out = torch.empty((B, K - 1, C), dtype=x.dtype, device=dev)
+    _run("gdn_short_conv", dev, _lib.gdn_short_conv, _ptr(x), *_strides(x, 2), _ptr(w), _ptr(bias), _ptr(state),
+         _ptr(state_out), _ptr(y), _ptr(lengths), B, T, C, K, int(bool(silu)), _DT[x.dtype])
+    return y, state_out
+
+
+def short_conv_step(x, w, bias, state, *, silu=True, lengths=None, out=None):
+    """One streaming call of short_conv (usually T = 1): `state` ([B,K-1,C],
+    x's dtype) is updated in place.  Returns y."""
+    return short_conv(x, w, bias, state, silu=silu, lengths=lengths, out=out, state_out=state)[0]
+
+
+def rotary_freqs(rot_dim, *, base=10000.0, scaling="none", factor=1.0, original_len=None, beta_fast=32.0,
+                 beta_slow=1.0, axes=None, device="cuda"):
+    """Table of the angles of `rotary`: (freqs, scale).
+
+    freqs: int64 [2, rot_dim/2] on `device`: each pair's angle per position as
+    a 64-bit fraction of a turn, and the position axis that it follows; scale:
+    the factor on the rotated channels (1 but for "yarn").
+      theta_j = base^(-2j/rot_dim)
+      scaling "linear": theta / factor;  "ntk": base * factor^(rot_dim/(rot_dim-2));
+      "yarn" (Peng et al. 2023): pairs that turn more than beta_fast times over
+      original_len positions keep theta, those below beta_slow take
+      theta / factor, a ramp between; scale = 0.1 ln(factor) + 1.
+      axes: channels per position axis (even, summing to rot_dim), for instance
+      (44, 42, 42) for frame, row and column; axis a of n_a channels has
+      theta_j = base^(-2j/n_a)."""
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be even and at least 2, got %d" % rot_dim)
+    if scaling not in ("none", "linear", "ntk", "yarn"):
+        raise ValueError("unknown scaling %r" % (scaling,))
+    if not base > 0 or not factor > 0:
+        raise ValueError("base and factor must be positive")
+    dims = [rot_dim] if axes is None else list(axes)
+    if sum(dims) != rot_dim or any(n < 2 or n % 2 for n in dims):
+        raise ValueError("axes must be even and sum to rot_dim (%d), got %s" % (rot_dim, dims))
+    scale = 1.0
+    theta, axis = [], []
+    for a, n in enumerate(dims):
+        b = float(base)
+        if scaling == "ntk":
+            if n == 2:
+                raise ValueError("ntk scaling needs more than one pair an axis")
+            b *= factor ** (n / (n - 2.0))
+        for j in range(n // 2):
+            th = b ** (-2.0 * j / n)
+            if scaling == "linear":
+                th /= factor
+            elif scaling == "yarn":
+                if original_len is None or not original_len > 0 or not beta_fast > beta_slow:
+                    raise ValueError("yarn scaling needs original_len > 0 and beta_fast > beta_slow")
+                ramp = (original_len * th / (2 * math.pi) - beta_slow) / (beta_fast - beta_slow)
+                ramp = min(1.0, max(0.0, ramp))
+                th = (1.0 - ramp) * th / factor + ramp * th
+            theta.append(th)
+            axis.append(a)
+    if scaling == "yarn":
+        scale = 0.1 * math.log(factor) + 1.0
+    turns = []
+    for th in theta:
+        p = int(round(Fraction(th) / _TWO_PI * 2 ** 64)) % 2 ** 64
+        turns.append(p - 2 ** 64 if p >= 2 ** 63 else p)
+    return torch.tensor([turns, axis], dtype=torch.int64, device=device), scale
+
+
+def rotary(q, k, pos, freqs, *, interleaved=False, scale=1.0, q_out=None, k_out=None):
+    """Rotary positions of q [B,T,Hq,d] and k [B,T,Hk,d] (k may be None) in one
+    pass: pair j of every head is turned by pos * theta_j.
+
+    q, k: fp32 or bf16, any strides (last dimension contiguous); pos: [B,T] or
+    [B,T,axes], int32 or int64, contiguous; freqs, scale: from rotary_freqs
+    (2 * freqs.shape[1] <= d channels are turned, the others pass through);
+    interleaved: pairs (2j, 2j+1), else (j, j + rot/2).  q_out / k_out: where
+    the results go (q / k itself: in place); new contiguous tensors by default.
+    Returns (q', k')."""
+    if q.dtype not in _DT:
+        raise ValueError("q must be float32 or bfloat16")
+    if q.dim() != 4 or (k is not None and k.dim() != 4):
+        raise ValueError("q and k must be [B, T, heads, d]")
+    B, T, Hq, d = q.shape
+    dev = q.device
+    _view(q, "q")
+    if k is not None:
+        _view(k, "k", q.dtype, (B, T, k.shape[2], d), dev)
+    if pos.dtype not in (torch.int32, torch.int64):
+        raise ValueError("pos must be int32 or int64")
+    axes = pos.shape[2] if pos.dim() == 3 else 1
+    _dense(pos, "pos", None, (B, T) if pos.dim() == 2 else (B, T, axes), dev)
+    _dense(freqs, "freqs", torch.int64, (2, freqs.shape[-1]), dev)
+    rot = 2 * freqs.shape[1]
+    if rot > d:
+        raise ValueError("freqs turn %d channels, the heads have %d" % (rot, d))
+    if q_out is None:
+        q_out = torch.empty((B, T, Hq, d), dtype=q.dtype, device=dev)
+    else:
+        _view(q_out, "q_out", q.dtype, q.shape, dev)
+    none = (0, 0, 0)
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty(tuple(k.shape), dtype=k.dtype, device=dev)
+        else:
+            _view(k_out, "k_out", k.dtype, k.shape, dev)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _run("gdn_rotary", dev, _lib.gdn_rotary, _ptr(q), _strides(q, 3), _ptr(q_out), _strides(q_out, 3), Hq, _ptr(k),
+         none if k is None else _strides(k, 3), _ptr(k_out), none if k is None else _strides(k_out, 3),
+         0 if k is None else k.shape[2], _ptr(pos), 64 if pos.dtype == torch.int64 else 32, axes, _ptr(freqs),
+         float(scale), B, T, d, rot, int(bool(interleaved)), _DT[q.dtype])
+    return q_out, k_out
+
+
+def ssm_workspace_size(B, T, H, G, dk, dv, dtype=torch.bfloat16) -> int:
+    return _lib.gdn_ssm_workspace_size(B, T, H, G, dk, dv, _DT[dtype])
+
+
+def ssm_scan(q, k, v, dt, A, D=None, dt_bias=None, state=None, *, softplus=True, lengths=None, return_state=True,
+             out=None, state_out=None, workspace=None):
+    """Selective state space scan (the scan without the erase term):
+    d_t = softplus(dt_t + dt_bias), S_t = exp(d_t A) S_{t-1} + d_t k_t v_t^T,
+    o_t = S_t^T q_t + D v_t.
+
+    q, k: [B,T,G,dk] (G groups, each shared by H/G heads), v: [B,T,H,dv], fp32
+    or bf16, any batch and token stride (multiples of 16 bytes); dt: [B,T,H]
+    fp32 or q's dtype, any batch and token stride; A (<= 0), D, dt_bias: [H]
+    fp32; state: [B,H,dk,dv] fp32 (None = zero); lengths: [B] int32, tokens of
+    each sequence of a padded batch.  Returns (o, final state) (the state None
+    if not asked), o in q's dtype.  A new o is zero behind a sequence's end, a
+    given `out` keeps what it held there."""
+    if q.dtype not in _DT:
+        raise ValueError("q must be float32 or bfloat16")
+    if q.dim() != 4 or v.dim() != 4 or dt.dim() != 3:
+        raise ValueError("q, k must be [B, T, G, dk], v [B, T, H, dv], dt [B, T, H]")
+    B, T, G, dk = q.shape
+    H, dv = v.shape[2], v.shape[3]
+    dev = q.device
+    _view(q, "q")
+    _view(k, "k", q.dtype, q.shape, dev)
+    _view(v, "v", q.dtype, (B, T, H, dv), dev)
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        _rows(t, name)
+    if dt.dtype not in (torch.float32, q.dtype):
+        raise ValueError("dt must be float32 or q's dtype")
+    _view(dt, "dt", None, (B, T, H), dev)
+    if G < 1 or H % G:
+        raise ValueError("the %d heads of v must be a multiple of the %d groups of q and k" % (H, G))
+    for t, name in ((A, "A"), (D, "D"), (dt_bias, "dt_bias")):
+        if t is not None:
+            _dense(t, name, torch.float32, (H,), dev)
+    if state is not None:
+        _dense(state, "state", torch.float32, (B, H, dk, dv), dev)
+    _lengths(lengths, B, dev)
+    o = _result(out, (B, T, H, dv), q.dtype, dev, lengths)
+    if state_out is not None:
+        _dense(state_out, "state_out", torch.float32, (B, H, dk, dv), dev)
+    elif return_state:
+        state_out = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+    ws, nbytes = _workspace(ssm_workspace_size(B, T, H, G, dk, dv, q.dtype), dev, workspace)
+    _run("gdn_ssm_scan", dev, _lib.gdn_ssm_scan, _ptr(q), _strides(q, 2), _ptr(k), _strides(k, 2), _ptr(v),
+         _strides(v, 2), _ptr(dt), _strides(dt, 2), _ptr(A), _ptr(D), _ptr(dt_bias), _ptr(state), _ptr(state_out),
+         _ptr(o), _ptr(lengths), B, T, H, G, dk, dv, int(bool(softplus)), _DT[q.dtype], _DT[dt.dtype], _ptr(ws),
+         nbytes)
+    return o, state_out
+
+
+def ssm_step(q, k, v, dt, A, state, D=None, dt_bias=None, *, softplus=True, lengths=None, out=None,
+             workspace=None):
+    """One streaming call of ssm_scan (usually T = 1): `state` ([B,H,dk,dv]
+    fp32) is updated in place.  Returns o."""
+    return ssm_scan(q, k, v, dt, A, D, dt_bias, state, softplus=softplus, lengths=lengths, out=out, state_out=state,
+                    workspace=workspace)[0]

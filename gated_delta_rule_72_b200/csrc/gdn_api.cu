@@ -12,6 +12,7 @@
 
 #include "../../include/gdn.h"
 #include "common.cuh"
+#include "host.cuh"
 #include "launch_stats.cuh"
 #include "simt_kernels.cuh"
 #include "tc_chain.cuh"
@@ -739,6 +740,12 @@ gdn_status noalloc_scratch(void **out) {
 
 }  // namespace
 
+namespace gdn {
+PFN_cuTensorMapEncodeTiled_v12000 driver_tensor_map_encoder() { return tensor_map_encoder(); }
+unsigned int *wait_timeout_counter() { return timeout_counter(); }
+int device_sm_count() { return sm_count(); }
+}  // namespace gdn
+
 extern "C" {
 
 gdn_status gdn_scan_causal(const void *q, const void *k, const void *v, const float *alpha,
@@ -816,10 +823,10 @@ const char *gdn_status_string(gdn_status s) {
     switch (s) {
         case GDN_OK: return "ok";
         case GDN_ERR_NULL: return "a required pointer is NULL";
-        case GDN_ERR_SHAPE: return "bad shape (B<1, H<1, T<0, size overflow, or overlapping state buffers)";
+        case GDN_ERR_SHAPE: return "bad shape (B<1, H<1, T<0, size overflow, overlapping strides or buffers)";
         case GDN_ERR_DTYPE: return "unknown dtype";
         case GDN_ERR_ALIGN: return "pointer not 16-byte aligned (workspace: 256-byte)";
-        case GDN_ERR_UNSUPPORTED: return "unsupported head dimension (dk, dv must be 64 or 128)";
+        case GDN_ERR_UNSUPPORTED: return "unsupported size (dk, dv must be 64 or 128; filter taps 2 to 4; rotary width even, at most 256)";
         case GDN_ERR_WORKSPACE: return "workspace smaller than gdn_workspace_size()";
         case GDN_ERR_CUDA: return "CUDA launch or copy failed";
     }

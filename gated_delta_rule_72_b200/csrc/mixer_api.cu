@@ -1,0 +1,343 @@
+// mixer_api.cu -- C-ABI entry points of the operators around the gated scan:
+// the short causal convolution, rotary positions and the selective state
+// space scan (argument checks and kernel dispatch).  See include/gdn.h.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/gdn.h"
+#include "common.cuh"
+#include "host.cuh"
+#include "launch_stats.cuh"
+#include "rotary.cuh"
+#include "short_conv.cuh"
+#include "ssm_token.cuh"
+
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+bool known(gdn_dtype d) { return d == GDN_F32 || d == GDN_BF16; }
+size_t esize(gdn_dtype d) { return d == GDN_F32 ? 4 : 2; }
+
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const char *p = static_cast<const char *>(a), *q = static_cast<const char *>(b);
+    return p && q && na && nb && p < q + nb && q < p + na;
+}
+// Bytes from the first to behind the last element of a [B, T, H, d] view.
+size_t span(int B, size_t bs, int T, size_t ts, int H, size_t hs, size_t d, size_t es) {
+    return ((size_t)(B - 1) * bs + (size_t)(T - 1) * ts + (size_t)(H - 1) * hs + d) * es;
+}
+
+// A [B, T, H, d] view, strides in elements.
+struct View {
+    const void *p;
+    int B;
+    size_t bs;
+    int T;
+    size_t ts;
+    int H;
+    size_t hs;
+    int d;
+    size_t row() const { return (size_t)(H - 1) * hs + d; }
+    size_t batch() const { return (size_t)(T - 1) * ts + row(); }
+    size_t all() const { return (size_t)(B - 1) * bs + batch(); }
+};
+
+// No two elements of a view share memory.
+bool distinct(const View &v) {
+    size_t n[3] = {(size_t)v.B, (size_t)v.T, (size_t)v.H};
+    const size_t st[3] = {v.bs, v.ts, v.hs};
+    size_t extent = v.d;
+    for (int pass = 0; pass < 3; ++pass) {
+        int m = -1;   // the smallest stride left
+        for (int i = 0; i < 3; ++i)
+            if (n[i] > 1 && (m < 0 || st[i] < st[m])) m = i;
+        if (m < 0) break;
+        if (st[m] < extent) return false;
+        extent += (n[m] - 1) * st[m];
+        n[m] = 1;
+    }
+    return true;
+}
+
+// Two views may share memory: their spans overlap and they are not disjoint
+// columns of the same rows (or of the same batch entries).
+bool clash(const View &x, const View &y, size_t es) {
+    if (!overlap(x.p, x.all() * es, y.p, y.all() * es)) return false;
+    const long long bytes = static_cast<const char *>(y.p) - static_cast<const char *>(x.p);
+    if (bytes % (long long)es) return true;
+    const long long off = bytes / (long long)es;
+    // [0, nx) and [off, off + ny) are disjoint in every period
+    auto apart = [off](size_t nx, size_t ny, size_t period) {
+        const long long p = (long long)period;
+        if (off <= -p || off >= p) return false;
+        const long long o = off < 0 ? off + p : off;
+        return o >= (long long)nx && o + (long long)ny <= p;
+    };
+    if (x.B > 1 && x.bs == y.bs && apart(x.batch(), y.batch(), x.bs)) return false;
+    if (x.T > 1 && x.ts == y.ts && x.ts > 0 && (x.B == 1 || (x.bs == y.bs && x.bs % x.ts == 0)) &&
+        apart(x.row(), y.row(), x.ts))
+        return false;
+    return true;
+}
+
+gdn_status launch_status() { return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }
+
+constexpr int kMaxTokens = 1 << 30;
+
+// ---------------------------------------------------------------------------
+// Short convolution
+// ---------------------------------------------------------------------------
+template <typename T, int K, int V, bool kSilu>
+gdn_status launch_conv(gdn::conv::Args a, int B, cudaStream_t s) {
+    using namespace gdn::conv;
+    const int cx = (a.C + kThreads * V - 1) / (kThreads * V);
+    // long tiles re-read fewer rows before them; shorter ones when a call
+    // would not fill the GPU with four blocks an SM
+    const long long want = 4ll * gdn::device_sm_count();
+    int tile = 64;
+    while (tile > kBatch && (long long)cx * B * ((a.T + tile - 1) / tile) < want) tile /= 2;
+    const int least = (a.T + 65534) / 65535;               // grid.y limit
+    if (tile < least) tile = (least + kBatch - 1) / kBatch * kBatch;
+    a.tile = tile;
+    const int ty = a.T > 0 ? (a.T + tile - 1) / tile : 1;
+    gdn::LaunchScope ls("short_conv", s);
+    conv_kernel<T, K, V, kSilu><<<dim3(cx, ty, B), kThreads, 0, s>>>(a);
+    return launch_status();
+}
+
+template <typename T, int K, int V>
+gdn_status conv_act(const gdn::conv::Args &a, int B, int silu, cudaStream_t s) {
+    return silu ? launch_conv<T, K, V, true>(a, B, s) : launch_conv<T, K, V, false>(a, B, s);
+}
+
+template <typename T, int K>
+gdn_status conv_vec(const gdn::conv::Args &a, int B, int silu, cudaStream_t s) {
+    constexpr int V = 16 / sizeof(T);
+    const bool vec = a.C % V == 0 && (a.T == 0 || (aligned(a.x, 16) && a.x_ts % V == 0 && a.x_bs % V == 0));
+    return vec ? conv_act<T, K, V>(a, B, silu, s) : conv_act<T, K, 1>(a, B, silu, s);
+}
+
+template <typename T>
+gdn_status conv_width(const gdn::conv::Args &a, int B, int K, int silu, cudaStream_t s) {
+    if (K == 2) return conv_vec<T, 2>(a, B, silu, s);
+    if (K == 3) return conv_vec<T, 3>(a, B, silu, s);
+    return conv_vec<T, 4>(a, B, silu, s);
+}
+
+// ---------------------------------------------------------------------------
+// Rotary positions
+// ---------------------------------------------------------------------------
+template <typename T, int V, bool kInter, bool kElem>
+gdn_status launch_rotary(const gdn::rope::Args &a, cudaStream_t s) {
+    using namespace gdn::rope;
+    const long long blocks = (a.rows + a.tok - 1) / a.tok;
+    gdn::LaunchScope ls("rotary", s);
+    rotary_kernel<T, V, kInter, kElem><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+    return launch_status();
+}
+
+template <typename T>
+gdn_status rotary_type(const gdn::rope::Args &a, int inter, cudaStream_t s) {
+    constexpr int V = 16 / sizeof(T);
+    bool vec = a.rot % V == 0 && (inter || (a.rot / 2) % V == 0) && (!a.copy || (a.d - a.rot) % V == 0);
+    const gdn::rope::Part *ps[2] = {&a.q, &a.k};
+    for (const gdn::rope::Part *p : ps)
+        if (p->heads) {
+            vec = vec && aligned(p->in, 16) && aligned(p->out, 16);
+            const size_t st[6] = {p->in_bs, p->in_ts, p->in_hs, p->out_bs, p->out_ts, p->out_hs};
+            for (size_t x : st) vec = vec && x % V == 0;
+        }
+    if (inter) return vec ? launch_rotary<T, V, true, false>(a, s) : launch_rotary<T, 2, true, true>(a, s);
+    return vec ? launch_rotary<T, V, false, false>(a, s) : launch_rotary<T, 1, false, true>(a, s);
+}
+
+// ---------------------------------------------------------------------------
+// Selective state space scan
+// ---------------------------------------------------------------------------
+struct Scan {
+    gdn::ssm::Args a;
+    int dk, dv;
+    gdn_dtype t, dt_t;
+    cudaStream_t stream;
+};
+
+template <int DK, int DV, int CW, typename T, typename Td>
+gdn_status launch_token(const Scan &c) {
+    gdn::LaunchScope ls("ssm_token", c.stream);
+    gdn::ssm::token_kernel<DK, DV, CW, T, Td>
+        <<<dim3(DV / CW, c.a.B * c.a.H), gdn::ssm::kTokThreads, 0, c.stream>>>(c.a);
+    return launch_status();
+}
+
+template <int DK, int DV, typename T, typename Td>
+gdn_status token_cols(const Scan &c) {
+    // whole heads when they fill the GPU twice, else slices of 32 columns
+    if ((long long)c.a.B * c.a.H >= 2ll * gdn::device_sm_count()) return launch_token<DK, DV, DV, T, Td>(c);
+    return launch_token<DK, DV, 32, T, Td>(c);
+}
+
+template <typename T, typename Td>
+gdn_status token_dims(const Scan &c) {
+    if (c.dk == 128) return c.dv == 128 ? token_cols<128, 128, T, Td>(c) : token_cols<128, 64, T, Td>(c);
+    return c.dv == 128 ? token_cols<64, 128, T, Td>(c) : token_cols<64, 64, T, Td>(c);
+}
+
+gdn_status run_scan(const Scan &c) {
+    if (c.t == GDN_F32) return token_dims<float, float>(c);
+    return c.dt_t == GDN_F32 ? token_dims<bf16, float>(c) : token_dims<bf16, bf16>(c);
+}
+
+bool scan_sizes(int B, int T, int H, int G) {
+    return B >= 1 && H >= 1 && G >= 1 && T >= 0 && T <= kMaxTokens && H % G == 0 && (long long)B * H <= 65535;
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn_status gdn_short_conv(const void *x, size_t x_batch_stride, size_t x_token_stride, const float *w,
+                          const float *bias, const void *state_in, void *state_out, void *y, const int *lengths,
+                          int B, int T, int C, int K, int silu, gdn_dtype dt, void *stream) {
+    if (!known(dt)) return GDN_ERR_DTYPE;
+    if (B < 1 || B > 65535 || T < 0 || T > kMaxTokens || C < 1 || C > kMaxTokens) return GDN_ERR_SHAPE;
+    if (K < 2 || K > 4) return GDN_ERR_UNSUPPORTED;
+    if (T == 0 && !state_out) return GDN_OK;
+    if (!w || (T > 0 && (!x || !y))) return GDN_ERR_NULL;
+    const size_t es = esize(dt);
+    if (!aligned(w, 4) || !aligned(bias, 4) || !aligned(lengths, 4) || !aligned(x, es)) return GDN_ERR_ALIGN;
+    if (!aligned(y, 16) || !aligned(state_in, 16) || !aligned(state_out, 16)) return GDN_ERR_ALIGN;
+    if (T > 0 && ((T > 1 && x_token_stride < (size_t)C) || (B > 1 && x_batch_stride < (size_t)C)))
+        return GDN_ERR_SHAPE;
+    const size_t nx = T > 0 ? span(B, x_batch_stride, T, x_token_stride, 1, 0, C, es) : 0;
+    const size_t ny = (size_t)B * T * C * es, ns = (size_t)B * (K - 1) * C * es;
+    if (overlap(y, ny, x, nx) || overlap(y, ny, state_in, ns) || overlap(y, ny, state_out, ns) ||
+        overlap(state_out, ns, x, nx) || (overlap(state_out, ns, state_in, ns) && state_out != state_in))
+        return GDN_ERR_SHAPE;
+    const gdn::conv::Args a{x, x_batch_stride, x_token_stride, w, bias, state_in, state_out, y, lengths, T, C, 0};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return dt == GDN_F32 ? conv_width<float>(a, B, K, silu, s) : conv_width<bf16>(a, B, K, silu, s);
+}
+
+gdn_status gdn_rotary(const void *q, size_t q_batch_stride, size_t q_token_stride, size_t q_head_stride, void *q_out,
+                      size_t q_out_batch_stride, size_t q_out_token_stride, size_t q_out_head_stride, int Hq,
+                      const void *k, size_t k_batch_stride, size_t k_token_stride, size_t k_head_stride, void *k_out,
+                      size_t k_out_batch_stride, size_t k_out_token_stride, size_t k_out_head_stride, int Hk,
+                      const void *pos, int pos_bits, int axes, const void *freqs, float scale, int B, int T, int d,
+                      int rot, int interleaved, gdn_dtype dt, void *stream) {
+    if (!known(dt)) return GDN_ERR_DTYPE;
+    if (pos_bits != 32 && pos_bits != 64) return GDN_ERR_DTYPE;
+    if (B < 1 || T < 0 || T > kMaxTokens || Hq < 1 || Hk < 0 || Hq > 65535 || Hk > 65535 || d < 2 || axes < 1 ||
+        axes > 8 || (long long)B * T > (1ll << 31))
+        return GDN_ERR_SHAPE;
+    if (rot < 2 || rot % 2 || rot > d || rot > gdn::rope::kMaxRot || d > 1024) return GDN_ERR_UNSUPPORTED;
+    if (!(scale == scale) || scale > 3.0e38f || scale < -3.0e38f) return GDN_ERR_SHAPE;
+    if (T == 0) return GDN_OK;
+    if (!q || !q_out || !pos || !freqs || (Hk > 0 && (!k || !k_out))) return GDN_ERR_NULL;
+    const size_t es = esize(dt);
+    const void *ps[4] = {q, q_out, Hk ? k : q, Hk ? k_out : q};
+    for (const void *p : ps)
+        if (!aligned(p, es)) return GDN_ERR_ALIGN;
+    if (!aligned(pos, pos_bits / 8) || !aligned(freqs, 8)) return GDN_ERR_ALIGN;
+    gdn::rope::Args a{};
+    a.q = {q, q_out, q_batch_stride, q_token_stride, q_head_stride, q_out_batch_stride, q_out_token_stride,
+           q_out_head_stride, Hq};
+    a.k = {k, k_out, k_batch_stride, k_token_stride, k_head_stride, k_out_batch_stride, k_out_token_stride,
+           k_out_head_stride, Hk};
+    // an output is its own input exactly (in place), or overlaps neither
+    // input; the two outputs do not overlap
+    const View in[2] = {{q, B, q_batch_stride, T, q_token_stride, Hq, q_head_stride, d},
+                        {k, B, k_batch_stride, T, k_token_stride, Hk, k_head_stride, d}};
+    const View out[2] = {{q_out, B, q_out_batch_stride, T, q_out_token_stride, Hq, q_out_head_stride, d},
+                         {k_out, B, k_out_batch_stride, T, k_out_token_stride, Hk, k_out_head_stride, d}};
+    const int np = Hk ? 2 : 1;
+    bool copy = false;
+    for (int i = 0; i < np; ++i) {
+        if (!distinct(out[i])) return GDN_ERR_SHAPE;
+        const bool inplace = out[i].p == in[i].p && out[i].bs == in[i].bs && out[i].ts == in[i].ts &&
+                             out[i].hs == in[i].hs;
+        copy = copy || (!inplace && rot < d);
+        for (int j = 0; j < np; ++j)
+            if (!(i == j && inplace) && clash(out[i], in[j], es)) return GDN_ERR_SHAPE;
+    }
+    if (np == 2 && clash(out[0], out[1], es)) return GDN_ERR_SHAPE;
+    a.pos = pos;
+    a.freqs = static_cast<const long long *>(freqs);
+    a.scale = scale;
+    a.rows = (long long)B * T;
+    a.T = T;
+    a.d = d;
+    a.rot = rot;
+    a.axes = axes;
+    a.pos64 = pos_bits == 64;
+    a.copy = copy;
+    // as many tokens a block as leave eight blocks an SM
+    const long long tok = a.rows / (8ll * gdn::device_sm_count());
+    a.tok = (int)(tok < 1 ? 1 : (tok > gdn::rope::kMaxTok ? gdn::rope::kMaxTok : tok));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return dt == GDN_F32 ? rotary_type<float>(a, interleaved, s) : rotary_type<bf16>(a, interleaved, s);
+}
+
+gdn_status gdn_ssm_scan(const void *q, size_t q_batch_stride, size_t q_token_stride, const void *k,
+                        size_t k_batch_stride, size_t k_token_stride, const void *v, size_t v_batch_stride,
+                        size_t v_token_stride, const void *dt, size_t dt_batch_stride, size_t dt_token_stride,
+                        const float *A, const float *D, const float *dt_bias, const float *state_in,
+                        float *state_out, void *o, const int *lengths, int B, int T, int H, int G, int dk, int dv,
+                        int softplus, gdn_dtype t, gdn_dtype dt_t, void *workspace, size_t ws_bytes, void *stream) {
+    (void)workspace;
+    (void)ws_bytes;
+    if (!known(t) || !known(dt_t) || (t == GDN_F32 && dt_t != GDN_F32)) return GDN_ERR_DTYPE;
+    if (!scan_sizes(B, T, H, G)) return GDN_ERR_SHAPE;
+    if (!((dk == 64 || dk == 128) && (dv == 64 || dv == 128))) return GDN_ERR_UNSUPPORTED;
+    if (T == 0 && !state_out) return GDN_OK;
+    const size_t es = esize(t), de = esize(dt_t);
+    if (!aligned(state_in, 16) || !aligned(state_out, 16)) return GDN_ERR_ALIGN;
+    const size_t ns = (size_t)B * H * dk * dv * 4;
+    if (overlap(state_in, ns, state_out, ns) && state_in != state_out) return GDN_ERR_SHAPE;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (T == 0) {
+        if (state_out == state_in) return GDN_OK;
+        const cudaError_t e = state_in ? cudaMemcpyAsync(state_out, state_in, ns, cudaMemcpyDeviceToDevice, s)
+                                       : cudaMemsetAsync(state_out, 0, ns, s);
+        return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    }
+    if (!q || !k || !v || !dt || !A || !o) return GDN_ERR_NULL;
+    const void *ps[4] = {q, k, v, o};
+    for (const void *p : ps)
+        if (!aligned(p, 16)) return GDN_ERR_ALIGN;
+    // whole 16-byte rows: tile copies need them
+    const size_t st[6] = {q_batch_stride, q_token_stride, k_batch_stride, k_token_stride, v_batch_stride,
+                          v_token_stride};
+    for (size_t x : st)
+        if (x * es % 16) return GDN_ERR_ALIGN;
+    if (!aligned(dt, de) || !aligned(A, 4) || !aligned(D, 4) || !aligned(dt_bias, 4) || !aligned(lengths, 4))
+        return GDN_ERR_ALIGN;
+    const size_t row[3] = {(size_t)G * dk, (size_t)G * dk, (size_t)H * dv};
+    for (int i = 0; i < 3; ++i)
+        if ((B > 1 && st[2 * i] < row[i]) || (T > 1 && st[2 * i + 1] < row[i])) return GDN_ERR_SHAPE;
+    if ((B > 1 && dt_batch_stride < (size_t)H) || (T > 1 && dt_token_stride < (size_t)H)) return GDN_ERR_SHAPE;
+    const size_t no = (size_t)B * T * H * dv * es;
+    const void *in[3] = {q, k, v};
+    for (int i = 0; i < 3; ++i) {
+        const size_t n = span(B, st[2 * i], T, st[2 * i + 1], 1, 0, row[i], es);
+        if (overlap(o, no, in[i], n) || overlap(state_out, ns, in[i], n)) return GDN_ERR_SHAPE;
+    }
+    const size_t nd = span(B, dt_batch_stride, T, dt_token_stride, 1, 0, H, de);
+    if (overlap(o, no, dt, nd) || overlap(state_out, ns, dt, nd) || overlap(o, no, state_in, ns) ||
+        overlap(o, no, state_out, ns))
+        return GDN_ERR_SHAPE;
+    Scan c{{q, k, v, dt, q_batch_stride, q_token_stride, k_batch_stride, k_token_stride, v_batch_stride,
+            v_token_stride, dt_batch_stride, dt_token_stride, A, D, dt_bias, state_in, state_out, o, lengths, B, T, H,
+            G, softplus},
+           dk, dv, t, dt_t, s};
+    return run_scan(c);
+}
+
+size_t gdn_ssm_workspace_size(int B, int T, int H, int G, int dk, int dv, gdn_dtype t) {
+    (void)B; (void)T; (void)H; (void)G; (void)dk; (void)dv; (void)t;
+    return 0;
+}
+
+}  // extern "C"

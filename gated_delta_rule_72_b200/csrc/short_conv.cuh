@@ -1,0 +1,138 @@
+// short_conv.cuh -- short causal convolution over time, one filter per
+// channel (depthwise), the inputs' last K-1 rows carried as a state:
+//   y[b,t,c] = act(bias[c] + sum_{j<K} w[c,j] x[b, t-(K-1)+j, c])
+// with x before token 0 read from the state (zero without one) and act the
+// identity or silu(y) = y / (1 + e^-y).
+//
+// HBM-bound: every x is read once and every y written once; K multiply-adds
+// and one silu per element stay below that (two special-function operations
+// an element, 16 per SM and cycle, are 0.7 of the time of the bytes at bf16).
+// A thread owns V consecutive channels (16 bytes) for a tile of tokens: the
+// filter and the last K-1 inputs stay in registers, and kBatch rows are
+// loaded before the first is used, so that a thread has kBatch independent
+// 16-byte loads in flight.  A tile re-reads the K-1 rows before it.  Rows or
+// bases that are not 16-byte aligned, and channel counts that are no multiple
+// of V, take the V = 1 form.
+//
+// The state out is written by the threads of the first tile, which are also
+// the only readers of the state in: each thread has read its channels' state
+// before it writes them, so the state may be updated in place.
+#pragma once
+
+#include "common.cuh"
+
+namespace gdn {
+namespace conv {
+
+constexpr int kThreads = 128;
+constexpr int kBatch = 8;      // rows loaded ahead
+
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Vec { T e[V]; };
+
+struct Args {
+    const void *x;
+    size_t x_bs, x_ts;         // strides of the batch and of the tokens, elements
+    const float *w, *bias;     // [C, K]; [C] or NULL
+    const void *state_in;      // [B, K-1, C] or NULL
+    void *state_out;           // [B, K-1, C] or NULL
+    void *y;                   // [B, T, C]
+    const int *lengths;        // [B] or NULL
+    int T, C, tile;            // tile: tokens per block, a multiple of kBatch
+};
+
+__device__ __forceinline__ float silu(float y) { return __fdividef(y, 1.f + __expf(-y)); }
+
+template <typename T, int K, int V, bool kSilu>
+__global__ void __launch_bounds__(kThreads)
+conv_kernel(const Args a)
+{
+    using Row = Vec<T, V>;
+    const int c = (blockIdx.x * kThreads + threadIdx.x) * V;
+    if (c >= a.C) return;
+    const int b = blockIdx.z;
+    int n = a.T;
+    if (a.lengths) n = min(max(a.lengths[b], 0), a.T);
+    const int t0 = blockIdx.y * a.tile;
+    if (t0 >= n && t0 > 0) return;
+    const T *x = static_cast<const T *>(a.x) + (size_t)b * a.x_bs + c;
+    T *y = static_cast<T *>(a.y) + (size_t)b * a.T * a.C + c;
+
+    float w[K][V], bias[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int j = 0; j < K; ++j) w[j][i] = a.w[(size_t)(c + i) * K + j];
+        bias[i] = a.bias ? a.bias[c + i] : 0.f;
+    }
+    // the K-1 rows before the tile, oldest first
+    float h[K - 1][V];
+    if (t0 == 0) {
+        Row s[K - 1];
+        const T *si = static_cast<const T *>(a.state_in);
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[j].e[i] = from_f32<T>(0.f);
+            if (si) s[j] = *reinterpret_cast<const Row *>(si + ((size_t)b * (K - 1) + j) * a.C + c);
+        }
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) h[j][i] = to_f32(s[j].e[i]);
+        if (a.state_out) {
+            T *so = static_cast<T *>(a.state_out);
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) {
+                // position n - (K-1) + j; negative ones are in the state in
+                const int p = n - (K - 1) + j;
+                Row r;
+                if (p >= 0) {
+                    r = *reinterpret_cast<const Row *>(x + (size_t)p * a.x_ts);
+                } else {
+#pragma unroll
+                    for (int m = 0; m < K - 1; ++m)
+                        if (m == p + K - 1) r = s[m];
+                }
+                *reinterpret_cast<Row *>(so + ((size_t)b * (K - 1) + j) * a.C + c) = r;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) {
+            const int p = t0 - (K - 1) + j;   // tiles are longer than K-1 rows
+            const Row r = *reinterpret_cast<const Row *>(x + (size_t)p * a.x_ts);
+#pragma unroll
+            for (int i = 0; i < V; ++i) h[j][i] = to_f32(r.e[i]);
+        }
+    }
+
+    const int t1 = min(n, t0 + a.tile);
+    for (int t = t0; t < t1; t += kBatch) {
+        Row r[kBatch];
+#pragma unroll
+        for (int m = 0; m < kBatch; ++m)
+            if (t + m < t1) r[m] = *reinterpret_cast<const Row *>(x + (size_t)(t + m) * a.x_ts);
+#pragma unroll
+        for (int m = 0; m < kBatch; ++m) {
+            if (t + m >= t1) break;
+            Row out;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float xi = to_f32(r[m].e[i]);
+                float acc = bias[i];
+#pragma unroll
+                for (int j = 0; j < K - 1; ++j) acc = fmaf(w[j][i], h[j][i], acc);
+                acc = fmaf(w[K - 1][i], xi, acc);
+#pragma unroll
+                for (int j = 0; j + 1 < K - 1; ++j) h[j][i] = h[j + 1][i];
+                h[K - 2][i] = xi;
+                out.e[i] = from_f32<T>(kSilu ? silu(acc) : acc);
+            }
+            *reinterpret_cast<Row *>(y + (size_t)(t + m) * a.C) = out;
+        }
+    }
+}
+
+}  // namespace conv
+}  // namespace gdn

@@ -80,7 +80,7 @@ typedef enum {
     GDN_ERR_SHAPE = -2,       /* B < 1, H < 1, T < 0, or a size overflows */
     GDN_ERR_DTYPE = -3,       /* dt or o_dt is not a gdn_dtype */
     GDN_ERR_ALIGN = -4,       /* a pointer is not 16-byte (workspace: 256-byte) aligned */
-    GDN_ERR_UNSUPPORTED = -5, /* dk or dv not in {64, 128} */
+    GDN_ERR_UNSUPPORTED = -5, /* dk or dv not in {64, 128}; filter or rotary width not offered */
     GDN_ERR_WORKSPACE = -6,   /* ws_bytes < gdn_workspace_size(...) */
     GDN_ERR_CUDA = -7         /* a CUDA launch or copy failed */
 } gdn_status;
@@ -284,6 +284,91 @@ GDN_API size_t gdn_vda_workspace_size(int B, int F, int U, int H, int dk, int dv
 GDN_API gdn_status gdn_readout_gate(const void *o, gdn_dtype o_dt, const void *z, gdn_dtype z_dt,
                                     const float *gamma, float eps, void *y, gdn_dtype y_dt,
                                     int B, int T, int H, int dv, void *stream);
+
+/*
+ * Operators around the scan: what makes its q, k and v (a short causal
+ * convolution, rotary positions) and the scan without the erase term (a
+ * selective state space scan).  Unlike the scans above their inputs may be
+ * views: batch, token (and head) strides are in ELEMENTS, the last dimension
+ * is contiguous.  Outputs are contiguous unless strides are given.
+ * lengths (device, [B] int32, or NULL) gives the tokens of each sequence of a
+ * padded batch, clamped to 0..T: inputs behind a sequence are not used (any
+ * value, NaN too), outputs behind it are left as they were, and the final
+ * state is the one after the sequence's own last token.
+ */
+
+/*
+ * gdn_short_conv -- short causal convolution over time, one filter of K taps
+ * (2, 3 or 4) per channel:
+ *   y[b,t,c] = act(bias[c] + sum_{j<K} w[c,j] x[b, t-(K-1)+j, c])
+ * act = silu if silu != 0, else the identity.  x [B, T, C] (strided), y
+ * [B, T, C] contiguous, both `dt`; w [C, K] and bias [C] (or NULL) fp32.
+ *   state_in   [B, K-1, C] `dt`: the K-1 inputs before token 0, oldest first
+ *              (NULL: zero)
+ *   state_out  receives the last K-1 inputs; NULL: not written; may be
+ *              state_in (in place), must not overlap it otherwise.
+ * y, state_in and state_out are 16-byte aligned, x to its element; y must not
+ * overlap x.  T = 0 passes the state through.  fp32 arithmetic, one rounding.
+ */
+GDN_API gdn_status gdn_short_conv(const void *x, size_t x_batch_stride, size_t x_token_stride, const float *w,
+                                  const float *bias, const void *state_in, void *state_out, void *y,
+                                  const int *lengths, int B, int T, int C, int K, int silu, gdn_dtype dt,
+                                  void *stream);
+
+/*
+ * gdn_rotary -- rotary positions of q and k in one pass.  Pair j < rot/2 of
+ * every head is turned by angle = pos * theta_j:
+ *   (x0, x1) <- scale * (x0 cos - x1 sin, x0 sin + x1 cos)
+ * with the pair at channels (2j, 2j+1) (interleaved != 0) or (j, j + rot/2);
+ * channels behind rot pass through unscaled.
+ *   q, k     [B, T, Hq, d], [B, T, Hk, d] `dt`, any batch, token and head
+ *            strides; k may be NULL with Hk = 0.  rot even, <= d, <= 256;
+ *            d <= 1024.
+ *   *_out    either exactly the input (same pointer and strides: in place) or
+ *            a buffer that overlaps neither input.
+ *   pos      [B, T, axes] contiguous, pos_bits 32 or 64 (signed); any value.
+ *   freqs    device int64 [2, rot/2]: row 0 round(theta_j / 2 pi * 2^64) mod
+ *            2^64 (the angle of one position in turns, fixed point), row 1
+ *            the axis of pos the pair follows (0 .. axes-1; clamped).
+ * The angle is exact modulo one turn, whatever the position; cos and sin are
+ * fp32.  axes <= 8.  T = 0 is a no-op.
+ */
+GDN_API gdn_status gdn_rotary(const void *q, size_t q_batch_stride, size_t q_token_stride, size_t q_head_stride,
+                              void *q_out, size_t q_out_batch_stride, size_t q_out_token_stride,
+                              size_t q_out_head_stride, int Hq, const void *k, size_t k_batch_stride,
+                              size_t k_token_stride, size_t k_head_stride, void *k_out, size_t k_out_batch_stride,
+                              size_t k_out_token_stride, size_t k_out_head_stride, int Hk, const void *pos,
+                              int pos_bits, int axes, const void *freqs, float scale, int B, int T, int d, int rot,
+                              int interleaved, gdn_dtype dt, void *stream);
+
+/*
+ * gdn_ssm_scan -- selective state space scan (the delta rule's scan without
+ * the erase term, its decay and write strength from one step size):
+ *   d_t = softplus(dt_t + dt_bias_h)  (softplus = 0: dt_t + dt_bias_h)
+ *   S_t = e^{d_t A_h} S_{t-1} + d_t k_t v_t^T ,   o_t = S_t^T q_t + D_h v_t
+ *   q, k     [B, T, G, dk] `t`: G groups, each shared by H / G heads
+ *   v, o     [B, T, H, dv] `t`; o contiguous
+ *   dt       [B, T, H] `dt_t`: fp32, or bf16 when t is bf16
+ *   A        [H] fp32, <= 0;  D, dt_bias [H] fp32 or NULL (zero); d_t >= 0
+ *   state_*  [B, H, dk, dv] fp32, as in gdn_scan_causal (state_out may be
+ *            state_in)
+ * Pointers and the strides of q, k and v (in bytes) are multiples of 16, dt
+ * is aligned to its element; dk, dv in {64, 128}; B * H <= 65535, H a
+ * multiple of G.  o must not overlap an input.  T = 0 passes the state
+ * through.  Values of A or d_t outside the stated ranges are not detected and
+ * give unspecified results, but never out-of-bounds accesses.  Step sizes,
+ * decays, sums and the state are fp32.
+ */
+GDN_API gdn_status gdn_ssm_scan(const void *q, size_t q_batch_stride, size_t q_token_stride, const void *k,
+                                size_t k_batch_stride, size_t k_token_stride, const void *v, size_t v_batch_stride,
+                                size_t v_token_stride, const void *dt, size_t dt_batch_stride,
+                                size_t dt_token_stride, const float *A, const float *D, const float *dt_bias,
+                                const float *state_in, float *state_out, void *o, const int *lengths, int B, int T,
+                                int H, int G, int dk, int dv, int softplus, gdn_dtype t, gdn_dtype dt_t,
+                                void *workspace, size_t ws_bytes, void *stream);
+/* gdn_ssm_workspace_size -- bytes of workspace gdn_ssm_scan needs (0 for
+ * arguments it would reject). */
+GDN_API size_t gdn_ssm_workspace_size(int B, int T, int H, int G, int dk, int dv, gdn_dtype t);
 
 /* gdn_status_string -- static, NUL-terminated description of a status. */
 GDN_API const char *gdn_status_string(gdn_status s);
