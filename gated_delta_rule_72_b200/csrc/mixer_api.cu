@@ -11,6 +11,7 @@
 #include "launch_stats.cuh"
 #include "rotary.cuh"
 #include "short_conv.cuh"
+#include "ssm_tc.cuh"
 #include "ssm_token.cuh"
 
 namespace {
@@ -185,7 +186,116 @@ gdn_status token_dims(const Scan &c) {
     return c.dv == 128 ? token_cols<64, 128, T, Td>(c) : token_cols<64, 64, T, Td>(c);
 }
 
-gdn_status run_scan(const Scan &c) {
+// ---------------------------------------------------------------------------
+// Tensor-core path of the scan (bf16)
+// ---------------------------------------------------------------------------
+// Calls of at most this many tokens run token by token.
+constexpr int kTokenCall = 32;
+// Fewest chunks of a segment.
+constexpr int kMinSegChunks = 2;
+
+bool use_tc(int T, gdn_dtype t) { return t == GDN_BF16 && T > kTokenCall; }
+
+size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// Head blocks (128 value columns: two heads of 64 that share a group, else one
+// head) and the segments of their walks: as many as leave one wave of CTAs.
+struct TcPlan {
+    int hb, nhb, nC, nseg, L;
+    size_t tails, decs, init, bytes;   // workspace offsets and size
+};
+TcPlan plan_tc(int B, int T, int H, int G, int dk, int dv) {
+    TcPlan p{};
+    p.hb = dv == 64 && (H / G) % 2 == 0 ? 2 : 1;
+    p.nhb = H / p.hb;
+    p.nC = (T + gdn::ssmtc::kTok - 1) / gdn::ssmtc::kTok;
+    int g = gdn::device_sm_count() / (B * p.nhb);
+    if (g > p.nC / kMinSegChunks) g = p.nC / kMinSegChunks;
+    if (g < 1) g = 1;
+    p.L = (p.nC + g - 1) / g;
+    p.nseg = (p.nC + p.L - 1) / p.L;
+    if (p.nseg > 1) {
+        const size_t bh = (size_t)B * H, st = (size_t)dk * dv * 4;
+        p.decs = round_up(bh * (p.nseg - 1) * st, 256);
+        p.init = p.decs + round_up(bh * (p.nseg - 1) * 4, 256);
+        p.bytes = p.init + round_up(bh * st, 256);
+    }
+    return p;
+}
+
+// [B, T, D] view as tiles of 64 columns x 128 tokens, 128B swizzle.
+bool encode_rows(CUtensorMap *m, const void *base, int B, size_t bs, int T, size_t ts, int D) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = gdn::driver_tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t sb = B > 1 ? bs * 2 : ts * 2;
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)T, (cuuint64_t)B, 1};
+    const cuuint64_t strides[3] = {ts * 2, sb, sb};
+    const cuuint32_t box[4] = {64, gdn::ssmtc::kTok, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DK, int DV, int HB>
+gdn_status launch_tc(const Scan &c, const TcPlan &pl, void *ws) {
+    using namespace gdn::ssmtc;
+    const gdn::ssm::Args &a = c.a;
+    CUtensorMap mq, mk, mv, mo;
+    const int D = a.H * DV;
+    if (!encode_rows(&mq, a.q, a.B, a.q_bs, a.T, a.q_ts, a.G * DK) ||
+        !encode_rows(&mk, a.k, a.B, a.k_bs, a.T, a.k_ts, a.G * DK) ||
+        !encode_rows(&mv, a.v, a.B, a.v_bs, a.T, a.v_ts, D) ||
+        !encode_rows(&mo, a.o, a.B, (size_t)a.T * D, a.T, D, D))
+        return GDN_ERR_CUDA;
+    Params p{};
+    p.a = a;
+    p.dt_f32 = c.dt_t == GDN_F32;
+    p.nhb = pl.nhb;
+    p.nseg = pl.nseg;
+    p.L = pl.L;
+    p.init = a.state_in;
+    p.err = gdn::wait_timeout_counter();
+    if (!p.err) return GDN_ERR_CUDA;
+    if (pl.nseg > 1) {
+        char *base = static_cast<char *>(ws);
+        float *tails = reinterpret_cast<float *>(base + pl.tails);
+        float *decs = reinterpret_cast<float *>(base + pl.decs);
+        float *copy = a.state_in && a.state_in == a.state_out ? reinterpret_cast<float *>(base + pl.init) : nullptr;
+        auto kern = tail_kernel<DK, DV, HB>;
+        constexpr int smem = TailSmem<DK, DV * HB>::kBytes;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            return GDN_ERR_CUDA;
+        gdn::LaunchScope ls("ssm_tail", c.stream);
+        kern<<<dim3(pl.nseg - 1, a.B * pl.nhb), kTailThreads, smem, c.stream>>>(mk, mv, p, tails, decs, copy);
+        if (launch_status() != GDN_OK) return GDN_ERR_CUDA;
+        p.tails = tails;
+        p.decs = decs;
+        if (copy) p.init = copy;
+    }
+    auto kern = walk_kernel<DK, DV, HB>;
+    constexpr int smem = Smem<DK, DV * HB>::kBytes;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return GDN_ERR_CUDA;
+    gdn::LaunchScope ls("ssm_walk", c.stream);
+    kern<<<dim3(pl.nseg, a.B * pl.nhb), kThreads, smem, c.stream>>>(mq, mk, mv, mo, p);
+    return launch_status();
+}
+
+template <int DK>
+gdn_status tc_dims(const Scan &c, const TcPlan &pl, void *ws) {
+    if (c.dv == 128) return launch_tc<DK, 128, 1>(c, pl, ws);
+    return pl.hb == 2 ? launch_tc<DK, 64, 2>(c, pl, ws) : launch_tc<DK, 64, 1>(c, pl, ws);
+}
+
+gdn_status run_scan(const Scan &c, void *ws, size_t ws_bytes) {
+    if (use_tc(c.a.T, c.t)) {
+        const TcPlan pl = plan_tc(c.a.B, c.a.T, c.a.H, c.a.G, c.dk, c.dv);
+        if (pl.bytes && !ws) return GDN_ERR_NULL;
+        if (pl.bytes && !aligned(ws, 256)) return GDN_ERR_ALIGN;
+        if (ws_bytes < pl.bytes) return GDN_ERR_WORKSPACE;
+        return c.dk == 128 ? tc_dims<128>(c, pl, ws) : tc_dims<64>(c, pl, ws);
+    }
     if (c.t == GDN_F32) return token_dims<float, float>(c);
     return c.dt_t == GDN_F32 ? token_dims<bf16, float>(c) : token_dims<bf16, bf16>(c);
 }
@@ -286,8 +396,6 @@ gdn_status gdn_ssm_scan(const void *q, size_t q_batch_stride, size_t q_token_str
                         const float *A, const float *D, const float *dt_bias, const float *state_in,
                         float *state_out, void *o, const int *lengths, int B, int T, int H, int G, int dk, int dv,
                         int softplus, gdn_dtype t, gdn_dtype dt_t, void *workspace, size_t ws_bytes, void *stream) {
-    (void)workspace;
-    (void)ws_bytes;
     if (!known(t) || !known(dt_t) || (t == GDN_F32 && dt_t != GDN_F32)) return GDN_ERR_DTYPE;
     if (!scan_sizes(B, T, H, G)) return GDN_ERR_SHAPE;
     if (!((dk == 64 || dk == 128) && (dv == 64 || dv == 128))) return GDN_ERR_UNSUPPORTED;
@@ -332,12 +440,12 @@ gdn_status gdn_ssm_scan(const void *q, size_t q_batch_stride, size_t q_token_str
             v_token_stride, dt_batch_stride, dt_token_stride, A, D, dt_bias, state_in, state_out, o, lengths, B, T, H,
             G, softplus},
            dk, dv, t, dt_t, s};
-    return run_scan(c);
+    return run_scan(c, workspace, ws_bytes);
 }
 
 size_t gdn_ssm_workspace_size(int B, int T, int H, int G, int dk, int dv, gdn_dtype t) {
-    (void)B; (void)T; (void)H; (void)G; (void)dk; (void)dv; (void)t;
-    return 0;
+    if (!known(t) || !scan_sizes(B, T, H, G) || !((dk == 64 || dk == 128) && (dv == 64 || dv == 128))) return 0;
+    return use_tc(T, t) ? plan_tc(B, T, H, G, dk, dv).bytes : 0;
 }
 
 }  // extern "C"
