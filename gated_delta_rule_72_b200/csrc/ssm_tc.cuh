@@ -78,14 +78,34 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
 }
-// Wait for a phase, for at most kWaitNs (the clock is read once in 64 polls).
-__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity) {
-    if (mbar_wait(bar, parity, 64)) return true;
+// One lane of a converged warp, in the form that lets the compiler keep MMA
+// operands in uniform registers: behind a plain `lane == 0` each MMA cost
+// 150-180 cycles to issue, 62 (its execution time at N = 128) behind this.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+// The slow part of a wait: until the phase completes, for at most kWaitNs (the
+// clock and the abort flag are read once in 64 polls).  Out of line: the roles
+// of a CTA run different code, and what is inlined at every wait pushes the
+// others out of the instruction cache.
+static __device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort_s,
+                                              unsigned int *err) {
     const unsigned long long t0 = global_ns();
-    do {
+    for (;;) {
         if (mbar_wait(bar, parity, 64)) return true;
-    } while (global_ns() - t0 < kWaitNs);
-    return false;
+        if (*abort_s) return false;
+        if (global_ns() - t0 >= kWaitNs) {
+            *abort_s = 1;
+            atomicAdd(err, 1u);
+            return false;
+        }
+    }
+}
+// Bounded wait; false when it, or another role's, gave up.
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t ph, volatile int *abort_s, unsigned int *err) {
+    return mbar_try_wait(bar, ph & 1u) || wait_slow(bar, ph & 1u, abort_s, err);
 }
 // D[tmem] (+)= A[tmem] * B[smem]: A is M x 16 bf16, two K elements a column.
 __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
@@ -226,14 +246,7 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     const uint32_t tmem = *tmem_s;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
 
-    // Bounded wait; false (and the abort flag) when it gives up or another role did.
-    auto wait = [&](uint64_t *bar, uint32_t ph) {
-        if (!wait_phase(bar, ph & 1u)) {
-            *abort_s = 1;
-            if (lane == 0) atomicAdd(p.err, 1u);
-        }
-        return *abort_s == 0;
-    };
+    auto wait = [&](uint64_t *bar, uint32_t ph) { return wait_phase(bar, ph, abort_s, p.err); };
     auto partial = [&](int c) { return (c0 + c + 1) * kTok > n; };          // chunk with tokens behind the end
     // its rows behind the end are other sequences' memory only when n < T
     auto own_rows = [&](int c) { return partial(c) && n < p.a.T; };
@@ -282,11 +295,15 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         __syncwarp();
     } else if (warp == 1) {
         // ============================ MMA issue =====================================
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t idG = idesc(128, 128, 1, 0, 0);
             constexpr uint32_t idR = idesc(128, W, 1, 0, 0);
             constexpr uint32_t idS = idesc(128, DK, 1, 1, 1);
             constexpr uint32_t idY = idesc(128, DV, 1, 0, 1);
+            const uint64_t dQ = sdesc_sw128(sbase + SM::kQ), dK = sdesc_sw128(sbase + SM::kK);
+            const uint64_t dS = sdesc_sw128(sbase + SM::kS), dKm = sdesc_sw128_mn(sbase + SM::kK, 16384);
+            const uint64_t dX = sdesc_sw128_mn(sbase + SM::kX, 16384), dWX = sdesc_sw128_mn(sbase + SM::kWX, 4096);
+            auto adv = [](uint64_t d, uint32_t bytes) { return d + (uint64_t)(bytes >> 4); };
             uint32_t wph = 0;      // quarters issued
             for (int c = 0; c < nch; ++c) {
                 if (!wait(kq_full, c)) break;
@@ -296,7 +313,7 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 #pragma unroll
                 for (int k = 0; k < DK / 16; ++k) {
                     const uint32_t o = (k >> 2) * 16384 + (k & 3) * 32;
-                    mma_bf16(tmem + cG, sdesc_sw128(sbase + SM::kQ + o), sdesc_sw128(sbase + SM::kK + o), idG, k > 0);
+                    mma_bf16(tmem + cG, adv(dQ, o), adv(dK, o), idG, k > 0);
                 }
                 mma_commit(g_full);
                 // R = Q S
@@ -305,21 +322,22 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < DK / 16; ++k)
-                    mma_bf16(tmem + cR, sdesc_sw128(sbase + SM::kQ + (k >> 2) * 16384 + (k & 3) * 32),
-                             sdesc_sw128(sbase + SM::kS + (k >> 2) * (W * 128) + (k & 3) * 32), idR, k > 0);
+                    mma_bf16(tmem + cR, adv(dQ, (k >> 2) * 16384 + (k & 3) * 32),
+                             adv(dS, (k >> 2) * (W * 128) + (k & 3) * 32), idR, k > 0);
                 mma_commit(r_done);
                 // dS, 32 tokens at a time
                 if (c > 0 && !wait(ds_free, c - 1)) break;
                 bool ok = true;
+#pragma unroll 1
                 for (int q = 0; q < 4; ++q, ++wph) {
                     if (!(ok = wait(&wx_ready[q & 1], wph >> 1))) break;
                     tc_fence_after();
-                    const uint32_t wx = sbase + SM::kWX + (q & 1) * 16384;
+                    const uint64_t wx = adv(dWX, (q & 1) * 16384);
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
-                        const uint64_t bk = sdesc_sw128_mn(sbase + SM::kK + (2 * q + s) * 2048, 16384);
-                        mma_bf16(tmem + cS, sdesc_sw128_mn(wx + s * 2048, 4096), bk, idS, q + s > 0);
-                        mma_bf16(tmem + cS, sdesc_sw128_mn(wx + 8192 + s * 2048, 4096), bk, idS, 1);
+                        const uint64_t bk = adv(dKm, (2 * q + s) * 2048);
+                        mma_bf16(tmem + cS, adv(wx, s * 2048), bk, idS, q + s > 0);
+                        mma_bf16(tmem + cS, adv(wx, 8192 + s * 2048), bk, idS, 1);
                     }
                     mma_commit(&wx_free[q & 1]);
                 }
@@ -329,13 +347,13 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 // Y = M V
                 if (!wait(m_ready, c)) break;
                 tc_fence_after();
+                const uint64_t dV = adv(dX, (c & 1) * SM::kXSlot);
 #pragma unroll
                 for (int h = 0; h < HB; ++h)
 #pragma unroll
                     for (int s = 0; s < 8; ++s)
                         mma_bf16_ta(tmem + cY + h * DV, tmem + cG + 32 * (s >> 1) + 16 * h + 8 * (s & 1),
-                                    sdesc_sw128_mn(sbase + SM::kX + (c & 1) * SM::kXSlot + h * 16384 + s * 2048, 16384),
-                                    idY, s > 0);
+                                    adv(dV, h * 16384 + s * 2048), idY, s > 0);
                 mma_commit(y_full);
             }
         }
@@ -412,7 +430,7 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             }
             if (!wait(g_full, c)) break;
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int pp = 0; pp < 2; ++pp) {
                 const int pc = u + 2 * pp;           // 32 tokens j of this piece
                 const uint32_t col = tmem + lane_base + cG + pc * 32;
@@ -470,7 +488,7 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             const int t = (c0 + c) * kTok + row;
             __nv_bfloat16 *orow = static_cast<__nv_bfloat16 *>(p.a.o) +
                                   (((size_t)b * p.a.T + t) * p.a.H + h0) * DV + u * NCOL;
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < NCOL; k += 16) {
                 const int col = u * NCOL + k;
                 float r[16], y[16];
@@ -572,6 +590,7 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 if (lane == 0) mbar_arrive(fixed);
                 if (!wait(fixed, 0)) break;          // every row is zero before any is read
             }
+#pragma unroll 1
             for (int q = 0; q < 4; ++q, ++wph) {
                 if (wph >= 2 && !(ok = wait(&wx_free[q & 1], (wph >> 1) - 1))) break;
                 const int r = q * 32 + lane;
@@ -704,12 +723,7 @@ tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_s;
-    auto wait = [&](uint64_t *bar, uint32_t ph) {
-        if (!wait_phase(bar, ph & 1u)) {
-            *abort_s = 1;
-            if (lane == 0) atomicAdd(p.err, 1u);
-        }
-    };
+    auto wait = [&](uint64_t *bar, uint32_t ph) { return wait_phase(bar, ph, abort_s, p.err); };
     constexpr uint32_t idS = idesc(128, DK, 1, 1, 1);
     // this thread's token of a chunk, and its head (threads 0-127: the first, 128-255: the second)
     const int hh = tid >> 7, j = tid & 127;
@@ -777,13 +791,13 @@ tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         fence_async_shared();
         __syncthreads();
         if (*abort_s) break;
-        if (tid == 0) {
+        if (warp == 0 && elect_one()) {
             tc_fence_after();
+            const uint64_t dK = sdesc_sw128_mn(sbase + SM::kK, 16384), dW = sdesc_sw128_mn(sbase + SM::kWX, 16384);
 #pragma unroll
             for (int s = 0; s < 8; ++s) {
-                const uint64_t bk = sdesc_sw128_mn(sbase + SM::kK + s * 2048, 16384);
-                mma_bf16(tmem, sdesc_sw128_mn(sbase + SM::kWX + s * 2048, 16384), bk, idS, steps + s > 0);
-                mma_bf16(tmem, sdesc_sw128_mn(sbase + SM::kWX + 32768 + s * 2048, 16384), bk, idS, 1);
+                mma_bf16(tmem, dW + s * 128, dK + s * 128, idS, steps + s > 0);
+                mma_bf16(tmem, dW + 2048 + s * 128, dK + s * 128, idS, 1);
             }
             mma_commit(done);
         }
