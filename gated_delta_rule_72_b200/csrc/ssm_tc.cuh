@@ -11,13 +11,13 @@
 //   M  = G * decay * d, lower triangle, bf16, written over G in TMEM
 //   R  = Q S                              [128 x W],   S a bf16 copy of the state
 //   Y  = M V                              [128 x W],   A operand from TMEM
-//   dS = (w V)^T K                        [W x d_k],   w V as a bf16 hi/lo pair
+//   dS = (w V)^T K                        [W x d_k],   w V as three bf16 terms
 //   o  = P(i, start) R + Y + D v ,   S <- P(end, start) S + dS  (fp32 registers)
 //
 // Precision.  q, k, v are exact bf16 operands, so G is exact to fp32; M and the
 // operand copy of S are rounded once to bf16 (o itself is bf16: the roundings of
 // the terms stay at the size of the output's own).  The state is fp32: its
-// update takes the weighted values as hi + lo = 16 significant bits.  Decays
+// update takes the weighted values as three bf16 terms (24 significant bits).  Decays
 // are products of factors in (0, 1] only: a row factor (from the start of the
 // row's 32-token block) times a column factor (to that start), each a sum of
 // log-decays that is summed directly, so nothing over- or underflows that the
@@ -35,8 +35,8 @@
 // end until the decay has gone to zero, and the walk of segment g starts from
 // the decayed sum of the contributions before it.
 //
-// Warps: 0 loads and stores (TMA), 1 issues every MMA, 2-3 make the decay
-// tables, 4-11 make M and the output, 12-19 the weighted values and the state.
+// Warps: 0 loads and stores (TMA), 1 issues every MMA, 2 makes the decay
+// tables, 3-10 make M and the output, 11-18 the weighted values and the state.
 #pragma once
 
 #include "sm100.cuh"
@@ -53,7 +53,7 @@ using gdn::tc2::swz128;
 using gdn::tc2::unpack_bf16;
 
 constexpr int kTok = 128;                  // tokens per chunk
-constexpr int kThreads = 640;
+constexpr int kThreads = 608;              // 19 warps: up to 104 registers a thread
 constexpr int kTailThreads = 256;
 constexpr unsigned long long kWaitNs = 1000000000ull;   // a wait gives up after 1 s
 constexpr float kLog2e = 1.4426950408889634f;
@@ -118,6 +118,47 @@ __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, r;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "sub.rn.f32x2 r, a, b;\n\t"
+        "mov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+// x = hi + mid + lo, three bf16 terms for 24 significant bits: hi and mid are
+// cut off (their rest is exact), lo is rounded.
+__device__ __forceinline__ void split3(float2 x, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
+    auto top = [](float v) { return __uint_as_float(__float_as_uint(v) & 0xffff0000u); };
+    auto pack = [](float2 v) { return __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632); };
+    hi = pack(x);
+    x = sub2(x, make_float2(top(x.x), top(x.y)));
+    mid = pack(x);
+    x = sub2(x, make_float2(top(x.x), top(x.y)));
+    lo = pack_bf16(x.x, x.y);
+}
+// Eight bf16 values times w as three terms of 16 bytes.
+__device__ __forceinline__ void weigh8(const uint4 &v, float w, uint4 &hi, uint4 &mid, uint4 &lo) {
+    const uint32_t *x = reinterpret_cast<const uint32_t *>(&v);
+    uint32_t *h = reinterpret_cast<uint32_t *>(&hi), *m = reinterpret_cast<uint32_t *>(&mid),
+             *l = reinterpret_cast<uint32_t *>(&lo);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split3(mul2(unpack_bf16(x[i]), make_float2(w, w)), h[i], m[i], l[i]);
+}
+
+// S += f x, x a column of stride `ld`, eight loads in flight.
+template <int N>
+__device__ __forceinline__ void add_scaled(float (&S)[N], float f, const float *x, int ld) {
+#pragma unroll
+    for (int k = 0; k < N; k += 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) S[k + i] = fmaf(f, x[(size_t)(k + i) * ld], S[k + i]);
+        asm volatile("" ::: "memory");   // keeps later loads from being hoisted into more registers
+    }
+}
+
 // Decay tables of one chunk and head.  Blocks of 32 tokens; c: log2 decay from
 // the block's start to the token (included).
 struct Table {
@@ -136,8 +177,9 @@ struct Smem {
     static constexpr int kX = 0;                              // 2 slots: v, then the output tile
     static constexpr int kK = kX + 2 * kXSlot;
     static constexpr int kQ = kK + (DK / 64) * 16384;
-    static constexpr int kWX = kQ + (DK / 64) * 16384;        // 2 x (hi 8 KB, lo 8 KB): 32 tokens x 128 columns
-    static constexpr int kS = kWX + 2 * 16384;                // [W][DK] bf16, blocks of 64 d_k
+    static constexpr int kWX = kQ + (DK / 64) * 16384;        // 2 x 3 terms of 32 tokens x 128 columns (8 KB)
+    static constexpr int kWXBuf = 3 * 8192;
+    static constexpr int kS = kWX + 2 * kWXBuf;               // [W][DK] bf16, blocks of 64 d_k
     static constexpr int kTab = kS + (DK / 64) * W * 128;     // [2][2] tables
     static constexpr int kBar = kTab + 4 * (int)sizeof(Table);
     static constexpr int kCtl = kBar + 256;
@@ -162,10 +204,9 @@ __device__ __forceinline__ float load_dt(const Params &p, int b, int t, int h) {
     return p.dt_f32 ? static_cast<const float *>(p.a.dt)[i] : to_f32(static_cast<const __nv_bfloat16 *>(p.a.dt)[i]);
 }
 
-// Step size and log2 decay of token t (0 behind the sequence's end n).
-__device__ __forceinline__ void gate(const Params &p, int b, int t, int n, int h, float A2, float bias, float &d,
-                                     float &la) {
-    d = t < n ? gdn::ssm::step_size(load_dt(p, b, t, h) + bias, p.a.softplus) : 0.f;
+// Step size and log2 decay of a token (zero behind the sequence's end).
+__device__ __forceinline__ void gate(const Params &p, float x, bool live, float A2, float &d, float &la) {
+    d = live ? gdn::ssm::step_size(x, p.a.softplus) : 0.f;
     la = fmaxf(d * A2, kMinLog);
 }
 
@@ -219,14 +260,14 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         mbar_init(y_staged, 8);
         mbar_init(r_done, 1);
         mbar_init(s_ready, 8);
-        mbar_init(&wx_ready[0], 8);
-        mbar_init(&wx_ready[1], 8);
+        mbar_init(&wx_ready[0], 4);
+        mbar_init(&wx_ready[1], 4);
         mbar_init(&wx_free[0], 1);
         mbar_init(&wx_free[1], 1);
         mbar_init(ds_full, 1);
         mbar_init(ds_free, 8);
-        mbar_init(&tab_full[0], HB);
-        mbar_init(&tab_full[1], HB);
+        mbar_init(&tab_full[0], 1);
+        mbar_init(&tab_full[1], 1);
         mbar_init(&tab_free[0], 16);
         mbar_init(&tab_free[1], 16);
         fence_mbar_init();
@@ -332,12 +373,13 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 for (int q = 0; q < 4; ++q, ++wph) {
                     if (!(ok = wait(&wx_ready[q & 1], wph >> 1))) break;
                     tc_fence_after();
-                    const uint64_t wx = adv(dWX, (q & 1) * 16384);
+                    const uint64_t wx = adv(dWX, (q & 1) * SM::kWXBuf);
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
                         const uint64_t bk = adv(dKm, (2 * q + s) * 2048);
                         mma_bf16(tmem + cS, adv(wx, s * 2048), bk, idS, q + s > 0);
                         mma_bf16(tmem + cS, adv(wx, 8192 + s * 2048), bk, idS, 1);
+                        mma_bf16(tmem + cS, adv(wx, 16384 + s * 2048), bk, idS, 1);
                     }
                     mma_commit(&wx_free[q & 1]);
                 }
@@ -358,20 +400,39 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             }
         }
         __syncwarp();
-    } else if (warp < 4) {
+    } else if (warp == 2) {
         // ============================ decay tables ==================================
-        if (warp - 2 < HB) {
-            const int h = h0 + warp - 2;
-            const float A2 = p.a.A[h] * kLog2e, bias = p.a.dt_bias ? p.a.dt_bias[h] : 0.f;
-            for (int c = 0; c < nch; ++c) {
-                float d[4], la[4], suf[4], cc[4], sum[4];
+        float A2[HB], bias[HB], raw[HB][4];
+#pragma unroll
+        for (int h = 0; h < HB; ++h) {
+            A2[h] = p.a.A[h0 + h] * kLog2e;
+            bias[h] = p.a.dt_bias ? p.a.dt_bias[h0 + h] : 0.f;
+        }
+        auto fetch = [&](int c) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int t = (c0 + c) * kTok + q * 32 + lane;
+#pragma unroll
+                for (int h = 0; h < HB; ++h) raw[h][q] = t < n ? load_dt(p, b, t, h0 + h) : 0.f;
+            }
+        };
+        if (nch > 0) fetch(0);
+        for (int c = 0; c < nch; ++c) {
+            float d[HB][4], la[HB][4];
+#pragma unroll
+            for (int h = 0; h < HB; ++h)
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    gate(p, b, (c0 + c) * kTok + q * 32 + lane, n, h, A2, bias, d[q], la[q]);
+                    gate(p, raw[h][q] + bias[h], (c0 + c) * kTok + q * 32 + lane < n, A2[h], d[h][q], la[h][q]);
+            if (c + 1 < nch) fetch(c + 1);
+            if (c >= 2 && !wait(&tab_free[c & 1], (c >> 1) - 1)) break;
+#pragma unroll
+            for (int h = 0; h < HB; ++h) {
+                float suf[4], cc[4], sum[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    cc[q] = la[q];
-                    suf[q] = __shfl_down_sync(0xffffffffu, la[q], 1);
+                    cc[q] = la[h][q];
+                    suf[q] = __shfl_down_sync(0xffffffffu, la[h][q], 1);
                     if (lane == 31) suf[q] = 0.f;
                 }
 #pragma unroll
@@ -385,18 +446,17 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     }
 #pragma unroll
                 for (int q = 0; q < 4; ++q) sum[q] = __shfl_sync(0xffffffffu, cc[q], 31);
-                if (c >= 2 && !wait(&tab_free[c & 1], (c >> 1) - 1)) break;
-                Table &tb = tabs[(c & 1) * 2 + warp - 2];
+                Table &tb = tabs[(c & 1) * 2 + h];
                 float post = 0.f;
 #pragma unroll
                 for (int q = 3; q >= 0; --q) {
-                    tb.w[q * 32 + lane] = d[q] * ex2(suf[q] + post);
+                    tb.w[q * 32 + lane] = d[h][q] * ex2(suf[q] + post);
                     tb.c[q * 32 + lane] = cc[q];
-                    tb.e[q * 32 + lane] = cc[q] - __log2f(d[q]);
+                    tb.e[q * 32 + lane] = cc[q] - __log2f(d[h][q]);
                     float gap = 0.f;
 #pragma unroll
                     for (int r = q + 1; r < 4; ++r) {
-                        tb.cf[cf_off(r) + q * 32 + lane] = d[q] * ex2(suf[q] + gap);
+                        tb.cf[cf_off(r) + q * 32 + lane] = d[h][q] * ex2(suf[q] + gap);
                         gap += sum[r];
                     }
                     post += sum[q];
@@ -408,13 +468,13 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     tb.pre[3] = sum[0] + sum[1] + sum[2];
                     tb.dec = ex2(post);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&tab_full[c & 1]);
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tab_full[c & 1]);
         }
-    } else if (warp < 12) {
+    } else if (warp < 11) {
         // ============================ M and the output ==============================
-        const int u = (warp >> 2) - 1;               // pieces u, u + 2; columns u W/2 ..
+        const int u = (warp - 3) >> 2;               // pieces u, u + 2; columns u W/2 ..
         const int row = quarter * 32 + lane;
         constexpr int NCOL = W / 2;
         const int hcol = (u * NCOL) / DV;            // this warp group's head (of HB) in the output
@@ -482,7 +542,7 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             __syncwarp();
             if (lane == 0) mbar_arrive(&tab_free[c & 1]);
             // ---- o = P(i, start) R + Y + D v, over v in its slot
-            if (!wait(y_full, c) || !wait(&x_full[c & 1], c >> 1)) break;
+            if (!wait(y_full, c)) break;
             tc_fence_after();
             const bool direct = own_rows(c);
             const int t = (c0 + c) * kTok + row;
@@ -495,17 +555,13 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 tmem_ld16(tmem + lane_base + cR + col, r);
                 tmem_ld16(tmem + lane_base + cY + col, y);
                 unsigned char *xs = smem + SM::kX + (c & 1) * SM::kXSlot + (col >> 6) * 16384;
+                const uint32_t o0 = swz128(row * 128 + (col & 63) * 2);
+                uint4 *slot[2] = {reinterpret_cast<uint4 *>(xs + o0), reinterpret_cast<uint4 *>(xs + (o0 ^ 16))};
+                const uint4 v[2] = {*slot[0], *slot[1]};
                 tmem_wait_ld();
-                if (k + 16 == NCOL) {                // R and Y are read out
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(y_free);
-                }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    uint4 *slot = reinterpret_cast<uint4 *>(xs + swz128(row * 128 + ((col & 63) + 8 * e) * 2));
-                    const uint4 v = *slot;
-                    const uint32_t vv[4] = {v.x, v.y, v.z, v.w};
+                    const uint32_t vv[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
                     uint32_t w[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -514,17 +570,21 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                         w[i] = pack_bf16(fmaf(D, x.x, fmaf(rs, r[j], y[j])), fmaf(D, x.y, fmaf(rs, r[j + 1], y[j + 1])));
                     }
                     const uint4 out = make_uint4(w[0], w[1], w[2], w[3]);
-                    if (!direct) *slot = out;
+                    if (!direct) *slot[e] = out;
                     else if (t < n) *reinterpret_cast<uint4 *>(orow + k + 8 * e) = out;
                 }
             }
+            tc_fence_before();
             fence_async_shared();
             __syncwarp();
-            if (lane == 0) mbar_arrive(y_staged);
+            if (lane == 0) {
+                mbar_arrive(y_free);                 // R and Y are read out
+                mbar_arrive(y_staged);
+            }
         }
     } else {
         // ================= weighted values and the state ============================
-        const int u = (warp >> 2) - 3;               // d_k half of the state; 16-column half of the values
+        const int u = (warp - 11) >> 2;              // d_k half of the state
         constexpr int NK = DK / 2;
         const int v = quarter * 32 + lane;           // value column of the state (TMEM lane)
         const bool live = v < W;
@@ -539,15 +599,13 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             for (float lg = 0.f; g >= 0; --g) {       // contributions of the segments before, latest first
                 const size_t ti = (size_t)(b * p.a.H + h0 + hv) * (p.nseg - 1) + g;
                 const float *src = p.tails + (ti * DK + u * NK) * DV + vcol;
-#pragma unroll
-                for (int k = 0; k < NK; ++k) S[k] = fmaf(f, src[(size_t)k * DV], S[k]);
+                add_scaled<NK>(S, f, src, DV);
                 lg += p.decs[ti];
                 f = ex2(lg);
                 if (lg < kForgetLog) break;
             }
             if (seg == 0 && p.init)                  // (segment 0's contribution holds it for the others)
-#pragma unroll
-                for (int k = 0; k < NK; ++k) S[k] = fmaf(f, p.init[sidx + (size_t)k * DV], S[k]);
+                add_scaled<NK>(S, f, p.init + sidx, DV);
         }
         auto stage_state = [&]() {
             if (live)
@@ -564,7 +622,8 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if (lane == 0) mbar_arrive(s_ready);
         };
         stage_state();
-        const int xcol = quarter * 32 + u * 16;      // this warp's 16 value columns
+        const int xcol = quarter * 32;               // this warp's 32 value columns; quarters u and u + 2 of the tokens
+        unsigned char *wx = smem + SM::kWX + u * SM::kWXBuf + (xcol >> 6) * 4096;
         uint32_t wph = 0;
         bool ok = true;
         for (int c = 0; c < nch && ok; ++c) {
@@ -575,7 +634,7 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 // rows behind the end: zero, so that nothing there (NaN too) enters a product
                 if (!wait(kq_full, c)) break;
                 const int first = n - (c0 + c) * kTok;
-                for (int i = (warp - 12) * 32 + lane; i < kTok * 8; i += 256) {
+                for (int i = (warp - 11) * 32 + lane; i < kTok * 8; i += 256) {
                     const int r = i >> 3, ch = (i & 7) * 16;
                     if (r < first) continue;
 #pragma unroll
@@ -591,31 +650,29 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 if (!wait(fixed, 0)) break;          // every row is zero before any is read
             }
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q, ++wph) {
-                if (wph >= 2 && !(ok = wait(&wx_free[q & 1], (wph >> 1) - 1))) break;
+            for (int q = u; q < 4; q += 2, ++wph) {
+                if (wph >= 1 && !(ok = wait(&wx_free[u], wph - 1))) break;
                 const int r = q * 32 + lane;
                 if (xcol < W) {
                     const float w = tb[xcol / DV].w[r];
-                    unsigned char *dst = smem + SM::kWX + (q & 1) * 16384 + (xcol >> 6) * 4096;
+#pragma unroll 1
+                    for (int e = 0; e < 4; e += 2) {
+                        const uint32_t o0 = swz128(lane * 128 + ((xcol & 63) + 8 * e) * 2), o1 = o0 ^ 16;
+                        const unsigned char *src = xs + (xcol >> 6) * 16384 + q * 4096;
+                        const uint4 x0 = *reinterpret_cast<const uint4 *>(src + o0);
+                        const uint4 x1 = *reinterpret_cast<const uint4 *>(src + o1);
+                        uint4 t[3];
+                        weigh8(x0, w, t[0], t[1], t[2]);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int cb = ((xcol & 63) + 8 * e) * 2;
-                        const uint4 x = *reinterpret_cast<const uint4 *>(xs + (xcol >> 6) * 16384 + swz128(r * 128 + cb));
-                        const uint32_t xx[4] = {x.x, x.y, x.z, x.w};
-                        uint32_t hi[4], lo[4];
+                        for (int i = 0; i < 3; ++i) *reinterpret_cast<uint4 *>(wx + o0 + i * 8192) = t[i];
+                        weigh8(x1, w, t[0], t[1], t[2]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 f = unpack_bf16(xx[i]);
-                            gdn::tc2::split2(w * f.x, w * f.y, hi[i], lo[i]);
-                        }
-                        *reinterpret_cast<uint4 *>(dst + swz128(lane * 128 + cb)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4 *>(dst + 8192 + swz128(lane * 128 + cb)) =
-                            make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        for (int i = 0; i < 3; ++i) *reinterpret_cast<uint4 *>(wx + o1 + i * 8192) = t[i];
                     }
                 }
                 fence_async_shared();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&wx_ready[q & 1]);
+                if (lane == 0) mbar_arrive(&wx_ready[u]);
             }
             if (!ok) break;
             const float dec = tb[hv].dec;
@@ -664,8 +721,8 @@ template <int DK, int W>
 struct TailSmem {
     static constexpr int kX = 0;                              // v: W/64 blocks
     static constexpr int kK = kX + (W / 64) * 16384;
-    static constexpr int kWX = kK + (DK / 64) * 16384;        // hi, lo: 128 tokens x 128 columns each
-    static constexpr int kW = kWX + 2 * 32768;                // weights [2][128]
+    static constexpr int kWX = kK + (DK / 64) * 16384;        // 3 terms of 128 tokens x 128 columns each
+    static constexpr int kW = kWX + 3 * 32768;                // weights [2][128]
     static constexpr int kRed = kW + 2 * kTok * 4;            // log-decay sums [2 heads][8 warps]
     static constexpr int kBar = kRed + 64;
     static constexpr int kCtl = kBar + 16;
@@ -737,7 +794,7 @@ tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     bool forgot = false;
     for (int c = c1 - 1; c >= c0; --c) {
         float d = 0.f, la = 0.f;
-        if (has) gate(p, b, c * kTok + j, n, h0 + hh, A2, bias, d, la);
+        if (has) gate(p, load_dt(p, b, c * kTok + j, h0 + hh) + bias, true, A2, d, la);   // whole chunks only
         // once everything is forgotten only the segment's decay is of interest: it is zero as well
         if (!forgot) {
             if (tid == 0) {
@@ -778,15 +835,10 @@ tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             const uint32_t off = (col >> 6) * 16384 + swz128(r * 128 + (col & 63) * 2);
             const uint4 x = *reinterpret_cast<const uint4 *>(smem + SM::kX + off);
             const float w = ws[(col / DV) * 128 + r];
-            const uint32_t xx[4] = {x.x, x.y, x.z, x.w};
-            uint32_t hi[4], lo[4];
+            uint4 t[3];
+            weigh8(x, w, t[0], t[1], t[2]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 f = unpack_bf16(xx[e]);
-                gdn::tc2::split2(w * f.x, w * f.y, hi[e], lo[e]);
-            }
-            *reinterpret_cast<uint4 *>(smem + SM::kWX + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(smem + SM::kWX + 32768 + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            for (int e = 0; e < 3; ++e) *reinterpret_cast<uint4 *>(smem + SM::kWX + e * 32768 + off) = t[e];
         }
         fence_async_shared();
         __syncthreads();
@@ -798,6 +850,7 @@ tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             for (int s = 0; s < 8; ++s) {
                 mma_bf16(tmem, dW + s * 128, dK + s * 128, idS, steps + s > 0);
                 mma_bf16(tmem, dW + 2048 + s * 128, dK + s * 128, idS, 1);
+                mma_bf16(tmem, dW + 4096 + s * 128, dK + s * 128, idS, 1);
             }
             mma_commit(done);
         }
