@@ -212,6 +212,8 @@ TcPlan plan_tc(int B, int T, int H, int G, int dk, int dv) {
     int g = gdn::device_sm_count() / (B * p.nhb);
     if (g > p.nC / kMinSegChunks) g = p.nC / kMinSegChunks;
     if (g < 1) g = 1;
+    const int least = (p.nC + gdn::ssmtc::kMaxSegChunks - 1) / gdn::ssmtc::kMaxSegChunks;
+    if (g < least) g = least;
     p.L = (p.nC + g - 1) / g;
     p.nseg = (p.nC + p.L - 1) / p.L;
     if (p.nseg > 1) {

@@ -36,7 +36,9 @@
 // the decayed sum of the contributions before it.
 //
 // Warps: 0 loads and stores (TMA), 1 issues every MMA, 2 makes the decay
-// tables, 3-10 make M and the output, 11-18 the weighted values and the state.
+// tables, 3-18 make M and the output, 19-26 the weighted values, 27-30 keep the
+// state.  Many warps with little code each: the roles share the instruction
+// caches, and a phase of one role is a chain of short dependent steps.
 #pragma once
 
 #include "sm100.cuh"
@@ -53,8 +55,10 @@ using gdn::tc2::swz128;
 using gdn::tc2::unpack_bf16;
 
 constexpr int kTok = 128;                  // tokens per chunk
-constexpr int kThreads = 608;              // 19 warps: up to 104 registers a thread
-constexpr int kTailThreads = 256;
+// Warps of the walk: 4 for the state, loads and stores, MMA issue, decay tables,
+// one idle, kCW for the weighted values, kMW for M and the output.
+constexpr int kCW = 4, kMW = 8;
+constexpr int kThreads = 32 * (8 + kCW + kMW);
 constexpr unsigned long long kWaitNs = 1000000000ull;   // a wait gives up after 1 s
 constexpr float kLog2e = 1.4426950408889634f;
 // Decays below 2^-256 are zero in fp32 many times over: per-token log-decays
@@ -139,24 +143,40 @@ __device__ __forceinline__ void split3(float2 x, uint32_t &hi, uint32_t &mid, ui
     x = sub2(x, make_float2(top(x.x), top(x.y)));
     lo = pack_bf16(x.x, x.y);
 }
-// Eight bf16 values times w as three terms of 16 bytes.
-__device__ __forceinline__ void weigh8(const uint4 &v, float w, uint4 &hi, uint4 &mid, uint4 &lo) {
-    const uint32_t *x = reinterpret_cast<const uint32_t *>(&v);
-    uint32_t *h = reinterpret_cast<uint32_t *>(&hi), *m = reinterpret_cast<uint32_t *>(&mid),
-             *l = reinterpret_cast<uint32_t *>(&lo);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) split3(mul2(unpack_bf16(x[i]), make_float2(w, w)), h[i], m[i], l[i]);
+// Four 8 x 8 blocks of 16-bit values, transposed: lane l gives the address of
+// row l % 8 of block l / 8 and gets column l / 4, rows 2 (l % 4) and one more.
+__device__ __forceinline__ void ldmatrix_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// 16 lanes x 16 columns: r[2 i + j] of lane l goes to TMEM lane 8 j + l / 4, column 4 i + l % 4.
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
-// S += f x, x a column of stride `ld`, eight loads in flight.
-template <int N>
-__device__ __forceinline__ void add_scaled(float (&S)[N], float f, const float *x, int ld) {
+// One warp's 32 tokens x 32 value columns of v times the tokens' weights, as
+// three terms of 16 TMEM columns (two tokens a column): src is this lane's row
+// (token) of the 128B-swizzled tile at the columns' start, w the weights of
+// tokens 2 (lane % 4), + 1 of each block of 8.
+__device__ __forceinline__ void weigh_block(uint32_t src, uint32_t dst, const float2 (&w)[4]) {
+#pragma unroll 1
+    for (int l = 0; l < 2; ++l) {    // 16 columns = lanes
+        uint32_t x[2][4], t[3][8];
 #pragma unroll
-    for (int k = 0; k < N; k += 8) {
+        for (int i = 0; i < 2; ++i) ldmatrix_t(src ^ (32 * l + 16 * i), x[i]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) S[k + i] = fmaf(f, x[(size_t)(k + i) * ld], S[k + i]);
-        asm volatile("" ::: "memory");   // keeps later loads from being hoisted into more registers
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                split3(mul2(unpack_bf16(x[i][k]), w[k]), t[0][2 * k + i], t[1][2 * k + i], t[2][2 * k + i]);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) tmem_st_16x128b_x4(dst + ((uint32_t)(16 * l) << 16) + 16 * i, t[i]);
     }
+    tmem_wait_st();
 }
 
 // Decay tables of one chunk and head.  Blocks of 32 tokens; c: log2 decay from
@@ -170,23 +190,6 @@ struct Table {
     float dec, pad[3];  // P(end, start)
 };
 __device__ __forceinline__ int cf_off(int b) { return 16 * b * (b - 1); }   // 0, 32, 96
-
-template <int DK, int W>
-struct Smem {
-    static constexpr int kXSlot = (W / 64) * 16384;
-    static constexpr int kX = 0;                              // 2 slots: v, then the output tile
-    static constexpr int kK = kX + 2 * kXSlot;
-    static constexpr int kQ = kK + (DK / 64) * 16384;
-    static constexpr int kWX = kQ + (DK / 64) * 16384;        // 2 x 3 terms of 32 tokens x 128 columns (8 KB)
-    static constexpr int kWXBuf = 3 * 8192;
-    static constexpr int kS = kWX + 2 * kWXBuf;               // [W][DK] bf16, blocks of 64 d_k
-    static constexpr int kTab = kS + (DK / 64) * W * 128;     // [2][2] tables
-    static constexpr int kBar = kTab + 4 * (int)sizeof(Table);
-    static constexpr int kCtl = kBar + 256;
-    static constexpr int kBytes = kCtl + 32;
-    static_assert(kBytes <= 232448, "shared memory budget");
-    static_assert(kS % 1024 == 0 && kWX % 1024 == 0 && kTab % 16 == 0, "alignment");
-};
 
 struct Params {
     gdn::ssm::Args a;
@@ -213,6 +216,22 @@ __device__ __forceinline__ void gate(const Params &p, float x, bool live, float 
 // ---------------------------------------------------------------------------
 // The walk
 // ---------------------------------------------------------------------------
+template <int DK, int W>
+struct Smem {
+    static constexpr int kXSlot = (W / 64) * 16384;
+    static constexpr int kKSlot = (DK / 64) * 16384;
+    static constexpr int kX = 0;                              // 2 slots: v, then the output tile
+    static constexpr int kK = kX + 2 * kXSlot;                // 2 slots
+    static constexpr int kQ = kK + 2 * kKSlot;
+    static constexpr int kS = kQ + kKSlot;                    // [W][DK] bf16, blocks of 64 d_k
+    static constexpr int kTab = kS + (DK / 64) * W * 128;     // [2][2] tables
+    static constexpr int kBar = kTab + 4 * (int)sizeof(Table);
+    static constexpr int kCtl = kBar + 256;
+    static constexpr int kBytes = kCtl + 32;
+    static_assert(kBytes <= 232448, "shared memory budget");
+    static_assert(kS % 1024 == 0 && kTab % 16 == 0, "alignment");
+};
+
 template <int DK, int DV, int HB>
 __global__ void __launch_bounds__(kThreads, 1)
 walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -220,7 +239,8 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 {
     constexpr int W = DV * HB;
     using SM = Smem<DK, W>;
-    constexpr uint32_t cG = 0, cR = 128, cY = 256, cS = 384;     // TMEM columns
+    // TMEM columns: G / M, R / Y, the state, two buffers of three 16-column terms of weighted values
+    constexpr uint32_t cG = 0, cY = 128, cS = 256, cW = 384;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t sbase = smem_u32(smem);
     if (sbase & 1023u) {
@@ -228,10 +248,23 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         return;
     }
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + SM::kBar);
-    uint64_t *x_full = bars, *kq_full = bars + 2, *kq_free = bars + 3, *fixed = bars + 4, *g_full = bars + 5,
-             *m_ready = bars + 6, *y_full = bars + 7, *y_free = bars + 8, *y_staged = bars + 9, *r_done = bars + 10,
-             *s_ready = bars + 11, *wx_ready = bars + 12, *wx_free = bars + 14, *ds_full = bars + 16,
-             *ds_free = bars + 17, *tab_full = bars + 18, *tab_free = bars + 20;
+    uint64_t *x_full = bars;           // [2] v loaded
+    uint64_t *k_full = bars + 2;       // [2] k loaded
+    uint64_t *k_free = bars + 4;       // [2] dS done with k
+    uint64_t *q_full = bars + 6;       // q loaded
+    uint64_t *r_done = bars + 7;       // R complete: q and the state's copy are read
+    uint64_t *fixed = bars + 8;        // rows behind the end are zero (last chunk)
+    uint64_t *g_full = bars + 9;       // G complete
+    uint64_t *m_ready = bars + 10;     // M written, R scaled
+    uint64_t *y_full = bars + 11;      // Y complete
+    uint64_t *y_free = bars + 12;      // Y read out
+    uint64_t *y_staged = bars + 13;    // output tile written
+    uint64_t *s_ready = bars + 14;     // state decayed in TMEM, its copy written
+    uint64_t *wx_ready = bars + 15;    // [2] weighted values written
+    uint64_t *wx_free = bars + 17;     // [2] ... and read
+    uint64_t *s_full = bars + 19;      // state updated
+    uint64_t *tab_full = bars + 20;    // [2] decay tables written
+    uint64_t *tab_free = bars + 22;    // [2] ... and read
     uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + SM::kCtl);
     volatile int *abort_s = reinterpret_cast<volatile int *>(smem + SM::kCtl + 4);
     Table *tabs = reinterpret_cast<Table *>(smem + SM::kTab);
@@ -248,28 +281,10 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     if (nch <= 0 && !last) return;
 
     if (tid == 0) {
-        mbar_init(&x_full[0], 1);
-        mbar_init(&x_full[1], 1);
-        mbar_init(kq_full, 1);
-        mbar_init(kq_free, 1);
-        mbar_init(fixed, 8);
-        mbar_init(g_full, 1);
-        mbar_init(m_ready, 8);
-        mbar_init(y_full, 1);
-        mbar_init(y_free, 8);
-        mbar_init(y_staged, 8);
-        mbar_init(r_done, 1);
-        mbar_init(s_ready, 8);
-        mbar_init(&wx_ready[0], 4);
-        mbar_init(&wx_ready[1], 4);
-        mbar_init(&wx_free[0], 1);
-        mbar_init(&wx_free[1], 1);
-        mbar_init(ds_full, 1);
-        mbar_init(ds_free, 8);
-        mbar_init(&tab_full[0], 1);
-        mbar_init(&tab_full[1], 1);
-        mbar_init(&tab_free[0], 16);
-        mbar_init(&tab_free[1], 16);
+        const uint8_t counts[24] = {1, 1, 1, 1, 1, 1, 1, 1, kCW, 1, kMW, 1, kMW, kMW, 4, 4, 4, 1, 1, 1, 1, 1,
+                                    4 + kCW + kMW, 4 + kCW + kMW};
+#pragma unroll
+        for (int i = 0; i < 24; ++i) mbar_init(bars + i, counts[i]);
         fence_mbar_init();
         *abort_s = 0;
         prefetch_tensormap(&tm_q);
@@ -292,7 +307,7 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     // its rows behind the end are other sequences' memory only when n < T
     auto own_rows = [&](int c) { return partial(c) && n < p.a.T; };
 
-    if (warp == 0) {
+    if (warp == 4) {
         // ============================ loads and stores ==============================
         if (lane == 0) {
             auto load_x = [&](int c) {
@@ -303,20 +318,30 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     tma_load_4d(smem + SM::kX + (c & 1) * SM::kXSlot + x * 16384, &tm_v, bar, h0 * DV + 64 * x,
                                 (c0 + c) * kTok, b, 0);
             };
-            auto load_kq = [&](int c) {
-                mbar_arrive_expect_tx(kq_full, 2 * (DK / 64) * 16384);
+            auto load_k = [&](int c) {
+                uint64_t *bar = &k_full[c & 1];
+                mbar_arrive_expect_tx(bar, SM::kKSlot);
 #pragma unroll
-                for (int x = 0; x < DK / 64; ++x) {
-                    tma_load_4d(smem + SM::kK + x * 16384, &tm_k, kq_full, grp * DK + 64 * x, (c0 + c) * kTok, b, 0);
-                    tma_load_4d(smem + SM::kQ + x * 16384, &tm_q, kq_full, grp * DK + 64 * x, (c0 + c) * kTok, b, 0);
-                }
+                for (int x = 0; x < DK / 64; ++x)
+                    tma_load_4d(smem + SM::kK + (c & 1) * SM::kKSlot + x * 16384, &tm_k, bar, grp * DK + 64 * x,
+                                (c0 + c) * kTok, b, 0);
             };
-            if (nch > 0) { load_kq(0); load_x(0); }
-            if (nch > 1) load_x(1);
+            auto load_q = [&](int c) {
+                mbar_arrive_expect_tx(q_full, SM::kKSlot);
+#pragma unroll
+                for (int x = 0; x < DK / 64; ++x)
+                    tma_load_4d(smem + SM::kQ + x * 16384, &tm_q, q_full, grp * DK + 64 * x, (c0 + c) * kTok, b, 0);
+            };
+            if (nch > 0) { load_k(0); load_q(0); load_x(0); }
+            if (nch > 1) { load_k(1); load_x(1); }
             for (int c = 0; c < nch; ++c) {
                 if (c + 1 < nch) {
-                    if (!wait(kq_free, c)) break;
-                    load_kq(c + 1);
+                    if (!wait(r_done, c)) break;
+                    load_q(c + 1);
+                }
+                if (c + 2 < nch) {
+                    if (!wait(&k_free[c & 1], c >> 1)) break;
+                    load_k(c + 2);
                 }
                 if (!wait(y_staged, c)) break;
                 if (!own_rows(c)) {
@@ -334,59 +359,58 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             bulk_wait_all();
         }
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp == 5) {
         // ============================ MMA issue =====================================
         if (elect_one()) {
             constexpr uint32_t idG = idesc(128, 128, 1, 0, 0);
             constexpr uint32_t idR = idesc(128, W, 1, 0, 0);
-            constexpr uint32_t idS = idesc(128, DK, 1, 1, 1);
+            constexpr uint32_t idS = idesc(128, DK, 1, 0, 1);
             constexpr uint32_t idY = idesc(128, DV, 1, 0, 1);
             const uint64_t dQ = sdesc_sw128(sbase + SM::kQ), dK = sdesc_sw128(sbase + SM::kK);
             const uint64_t dS = sdesc_sw128(sbase + SM::kS), dKm = sdesc_sw128_mn(sbase + SM::kK, 16384);
-            const uint64_t dX = sdesc_sw128_mn(sbase + SM::kX, 16384), dWX = sdesc_sw128_mn(sbase + SM::kWX, 4096);
+            const uint64_t dX = sdesc_sw128_mn(sbase + SM::kX, 16384);
             auto adv = [](uint64_t d, uint32_t bytes) { return d + (uint64_t)(bytes >> 4); };
             uint32_t wph = 0;      // quarters issued
             for (int c = 0; c < nch; ++c) {
-                if (!wait(kq_full, c)) break;
+                const uint32_t ks = (c & 1) * SM::kKSlot;
+                if (!wait(q_full, c) || !wait(&k_full[c & 1], c >> 1)) break;
                 if (partial(c) && !wait(fixed, 0)) break;
                 if (c > 0 && !wait(y_full, c - 1)) break;                     // M (over G) has been read
                 tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < DK / 16; ++k) {
                     const uint32_t o = (k >> 2) * 16384 + (k & 3) * 32;
-                    mma_bf16(tmem + cG, adv(dQ, o), adv(dK, o), idG, k > 0);
+                    mma_bf16(tmem + cG, adv(dQ, o), adv(dK, ks + o), idG, k > 0);
                 }
                 mma_commit(g_full);
-                // R = Q S
+                // R = Q S, over the output before
                 if (!wait(s_ready, c)) break;
                 if (c > 0 && !wait(y_free, c - 1)) break;
                 tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < DK / 16; ++k)
-                    mma_bf16(tmem + cR, adv(dQ, (k >> 2) * 16384 + (k & 3) * 32),
+                    mma_bf16(tmem + cY, adv(dQ, (k >> 2) * 16384 + (k & 3) * 32),
                              adv(dS, (k >> 2) * (W * 128) + (k & 3) * 32), idR, k > 0);
                 mma_commit(r_done);
-                // dS, 32 tokens at a time
-                if (c > 0 && !wait(ds_free, c - 1)) break;
+                // S += dS, 32 tokens at a time
                 bool ok = true;
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q, ++wph) {
                     if (!(ok = wait(&wx_ready[q & 1], wph >> 1))) break;
                     tc_fence_after();
-                    const uint64_t wx = adv(dWX, (q & 1) * SM::kWXBuf);
+                    const uint32_t wx = tmem + cW + (q & 1) * 48;
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
-                        const uint64_t bk = adv(dKm, (2 * q + s) * 2048);
-                        mma_bf16(tmem + cS, adv(wx, s * 2048), bk, idS, q + s > 0);
-                        mma_bf16(tmem + cS, adv(wx, 8192 + s * 2048), bk, idS, 1);
-                        mma_bf16(tmem + cS, adv(wx, 16384 + s * 2048), bk, idS, 1);
+                        const uint64_t bk = adv(dKm, ks + (2 * q + s) * 2048);
+#pragma unroll
+                        for (int t = 0; t < 3; ++t) mma_bf16_ta(tmem + cS, wx + 16 * t + 8 * s, bk, idS, 1);
                     }
                     mma_commit(&wx_free[q & 1]);
                 }
                 if (!ok) break;
-                mma_commit(ds_full);
-                mma_commit(kq_free);
-                // Y = M V
+                mma_commit(s_full);
+                mma_commit(&k_free[c & 1]);
+                // Y = scaled R + M V
                 if (!wait(m_ready, c)) break;
                 tc_fence_after();
                 const uint64_t dV = adv(dX, (c & 1) * SM::kXSlot);
@@ -395,12 +419,12 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 #pragma unroll
                     for (int s = 0; s < 8; ++s)
                         mma_bf16_ta(tmem + cY + h * DV, tmem + cG + 32 * (s >> 1) + 16 * h + 8 * (s & 1),
-                                    adv(dV, h * 16384 + s * 2048), idY, s > 0);
+                                    adv(dV, h * 16384 + s * 2048), idY, 1);
                 mma_commit(y_full);
             }
         }
         __syncwarp();
-    } else if (warp == 2) {
+    } else if (warp == 6) {
         // ============================ decay tables ==================================
         float A2[HB], bias[HB], raw[HB][4];
 #pragma unroll
@@ -472,46 +496,44 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             __syncwarp();
             if (lane == 0) mbar_arrive(&tab_full[c & 1]);
         }
-    } else if (warp < 11) {
+    } else if (warp >= 8 + kCW) {
         // ============================ M and the output ==============================
-        const int u = (warp - 3) >> 2;               // pieces u, u + 2; columns u W/2 ..
+        constexpr int NG = kMW / 4;                  // warp groups
+        const int u = (warp - 8 - kCW) >> 2;         // tokens 32 u .. of M (and every NG-th block), columns u NCOL ..
         const int row = quarter * 32 + lane;
-        constexpr int NCOL = W / 2;
+        constexpr int NCOL = W / NG;
         const int hcol = (u * NCOL) / DV;            // this warp group's head (of HB) in the output
         const float D = p.a.D ? p.a.D[h0 + hcol] : 0.f;
+        const uint32_t ycol = tmem + lane_base + cY + u * NCOL;
+                const uint32_t o0 = ((u * NCOL) >> 6) * 16384 + swz128(row * 128 + ((u * NCOL) & 63) * 2);
         for (int c = 0; c < nch; ++c) {
             const Table *tb = tabs + (c & 1) * 2;
             if (!wait(&tab_full[c & 1], c >> 1)) break;
-            float ci[HB], rf[HB];
-#pragma unroll
-            for (int h = 0; h < HB; ++h) {
-                ci[h] = tb[h].c[row];
-                rf[h] = ex2(ci[h]);
-            }
+            const float rs = ex2(tb[hcol].pre[quarter] + tb[hcol].c[row]);
             if (!wait(g_full, c)) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int pp = 0; pp < 2; ++pp) {
-                const int pc = u + 2 * pp;           // 32 tokens j of this piece
-                const uint32_t col = tmem + lane_base + cG + pc * 32;
+            for (int pc = u; pc < 4; pc += NG) {
+                const uint32_t gcol = tmem + lane_base + cG + pc * 32;
                 float g[32];
                 if (pc <= quarter) {
-                    tmem_ld16(col, g);
-                    tmem_ld16(col + 16, g + 16);
+                    tmem_ld16(gcol, g);
+                    tmem_ld16(gcol + 16, g + 16);
                     tmem_wait_ld();
                 }
-#pragma unroll
+#pragma unroll 1
                 for (int h = 0; h < HB; ++h) {
-                    float m[16];                     // packed pairs
+                    const float ci = tb[h].c[row];
+                    float m[16];                         // packed pairs
                     if (pc < quarter) {
                         const float4 *cf = reinterpret_cast<const float4 *>(tb[h].cf + cf_off(quarter) + pc * 32);
-                        const float2 r2 = make_float2(rf[h], rf[h]);
+                        const float rf = ex2(ci);
+                        const float2 r2 = make_float2(rf, rf);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             const float4 f = cf[j];
                             const float2 x = mul2(make_float2(g[4 * j], g[4 * j + 1]), mul2(make_float2(f.x, f.y), r2));
-                            const float2 y =
-                                mul2(make_float2(g[4 * j + 2], g[4 * j + 3]), mul2(make_float2(f.z, f.w), r2));
+                            const float2 y = mul2(make_float2(g[4 * j + 2], g[4 * j + 3]), mul2(make_float2(f.z, f.w), r2));
                             m[2 * j] = __uint_as_float(pack_bf16(x.x, x.y));
                             m[2 * j + 1] = __uint_as_float(pack_bf16(y.x, y.y));
                         }
@@ -520,10 +542,10 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             const float4 e = ej[j];
-                            const float x0 = 4 * j <= lane ? g[4 * j] * ex2(ci[h] - e.x) : 0.f;
-                            const float x1 = 4 * j + 1 <= lane ? g[4 * j + 1] * ex2(ci[h] - e.y) : 0.f;
-                            const float x2 = 4 * j + 2 <= lane ? g[4 * j + 2] * ex2(ci[h] - e.z) : 0.f;
-                            const float x3 = 4 * j + 3 <= lane ? g[4 * j + 3] * ex2(ci[h] - e.w) : 0.f;
+                            const float x0 = 4 * j <= lane ? g[4 * j] * ex2(ci - e.x) : 0.f;
+                            const float x1 = 4 * j + 1 <= lane ? g[4 * j + 1] * ex2(ci - e.y) : 0.f;
+                            const float x2 = 4 * j + 2 <= lane ? g[4 * j + 2] * ex2(ci - e.z) : 0.f;
+                            const float x3 = 4 * j + 3 <= lane ? g[4 * j + 3] * ex2(ci - e.w) : 0.f;
                             m[2 * j] = __uint_as_float(pack_bf16(x0, x1));
                             m[2 * j + 1] = __uint_as_float(pack_bf16(x2, x3));
                         }
@@ -531,32 +553,42 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 #pragma unroll
                         for (int j = 0; j < 16; ++j) m[j] = 0.f;
                     }
-                    tmem_st16(col + 16 * h, m);
+                    tmem_st16(gcol + 16 * h, m);
                 }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tab_free[c & 1]);
+            // ---- R <- P(i, start) R
+            if (!wait(r_done, c)) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int k = 0; k < NCOL; k += 16) {
+                float r[16];
+                tmem_ld16(ycol + k, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    const float2 x = mul2(make_float2(r[i], r[i + 1]), make_float2(rs, rs));
+                    r[i] = x.x;
+                    r[i + 1] = x.y;
+                }
+                tmem_st16(ycol + k, r);
             }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(m_ready);
-            const float rs = ex2(tb[hcol].pre[quarter] + tb[hcol].c[row]);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&tab_free[c & 1]);
-            // ---- o = P(i, start) R + Y + D v, over v in its slot
+            // ---- o = Y + D v, over v in its slot
             if (!wait(y_full, c)) break;
             tc_fence_after();
             const bool direct = own_rows(c);
-            const int t = (c0 + c) * kTok + row;
-            __nv_bfloat16 *orow = static_cast<__nv_bfloat16 *>(p.a.o) +
-                                  (((size_t)b * p.a.T + t) * p.a.H + h0) * DV + u * NCOL;
+            unsigned char *xs = smem + SM::kX + (c & 1) * SM::kXSlot;
 #pragma unroll 1
             for (int k = 0; k < NCOL; k += 16) {
-                const int col = u * NCOL + k;
-                float r[16], y[16];
-                tmem_ld16(tmem + lane_base + cR + col, r);
-                tmem_ld16(tmem + lane_base + cY + col, y);
-                unsigned char *xs = smem + SM::kX + (c & 1) * SM::kXSlot + (col >> 6) * 16384;
-                const uint32_t o0 = swz128(row * 128 + (col & 63) * 2);
-                uint4 *slot[2] = {reinterpret_cast<uint4 *>(xs + o0), reinterpret_cast<uint4 *>(xs + (o0 ^ 16))};
+                float y[16];
+                tmem_ld16(ycol + k, y);
+                uint4 *slot[2] = {reinterpret_cast<uint4 *>(xs + (o0 ^ (2 * k))),
+                                  reinterpret_cast<uint4 *>(xs + (o0 ^ (2 * k) ^ 16))};
                 const uint4 v[2] = {*slot[0], *slot[1]};
                 tmem_wait_ld();
 #pragma unroll
@@ -567,64 +599,36 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     for (int i = 0; i < 4; ++i) {
                         const float2 x = unpack_bf16(vv[i]);
                         const int j = 8 * e + 2 * i;
-                        w[i] = pack_bf16(fmaf(D, x.x, fmaf(rs, r[j], y[j])), fmaf(D, x.y, fmaf(rs, r[j + 1], y[j + 1])));
+                        w[i] = pack_bf16(fmaf(D, x.x, y[j]), fmaf(D, x.y, y[j + 1]));
                     }
                     const uint4 out = make_uint4(w[0], w[1], w[2], w[3]);
-                    if (!direct) *slot[e] = out;
-                    else if (t < n) *reinterpret_cast<uint4 *>(orow + k + 8 * e) = out;
+                    if (!direct) {
+                        *slot[e] = out;
+                    } else {
+                        const int t = (c0 + c) * kTok + row;
+                        if (t < n)
+                            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.a.o) +
+                                                       (((size_t)b * p.a.T + t) * p.a.H + h0) * DV + u * NCOL + k +
+                                                       8 * e) = out;
+                    }
                 }
             }
-            tc_fence_before();
             fence_async_shared();
+            tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(y_free);                 // R and Y are read out
+                mbar_arrive(y_free);
                 mbar_arrive(y_staged);
             }
         }
-    } else {
-        // ================= weighted values and the state ============================
-        const int u = (warp - 11) >> 2;              // d_k half of the state
-        constexpr int NK = DK / 2;
-        const int v = quarter * 32 + lane;           // value column of the state (TMEM lane)
-        const bool live = v < W;
-        const int hv = v / DV < HB ? v / DV : 0, vcol = v % DV;
-        const size_t sidx = ((size_t)(b * p.a.H + h0 + hv) * DK + u * NK) * DV + vcol;
-        float S[NK];
-#pragma unroll
-        for (int k = 0; k < NK; ++k) S[k] = 0.f;
-        if (live) {
-            float f = 1.f;
-            int g = seg - 1;
-            for (float lg = 0.f; g >= 0; --g) {       // contributions of the segments before, latest first
-                const size_t ti = (size_t)(b * p.a.H + h0 + hv) * (p.nseg - 1) + g;
-                const float *src = p.tails + (ti * DK + u * NK) * DV + vcol;
-                add_scaled<NK>(S, f, src, DV);
-                lg += p.decs[ti];
-                f = ex2(lg);
-                if (lg < kForgetLog) break;
-            }
-            if (seg == 0 && p.init)                  // (segment 0's contribution holds it for the others)
-                add_scaled<NK>(S, f, p.init + sidx, DV);
-        }
-        auto stage_state = [&]() {
-            if (live)
-#pragma unroll
-                for (int k = 0; k < NK; k += 8) {
-                    const int kk = u * NK + k;
-                    const uint4 x = make_uint4(pack_bf16(S[k], S[k + 1]), pack_bf16(S[k + 2], S[k + 3]),
-                                               pack_bf16(S[k + 4], S[k + 5]), pack_bf16(S[k + 6], S[k + 7]));
-                    *reinterpret_cast<uint4 *>(smem + SM::kS + (kk >> 6) * (W * 128) +
-                                               swz128(v * 128 + (kk & 63) * 2)) = x;
-                }
-            fence_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(s_ready);
-        };
-        stage_state();
-        const int xcol = quarter * 32;               // this warp's 32 value columns; quarters u and u + 2 of the tokens
-        unsigned char *wx = smem + SM::kWX + u * SM::kWXBuf + (xcol >> 6) * 4096;
-        uint32_t wph = 0;
+    } else if (warp >= 8) {
+        // ============================ weighted values ===============================
+        // This warp's 32 value columns are its 32 TMEM lanes: the values come out
+        // of shared memory transposed (8 x 8 blocks), and the blocks of 8 tokens
+        // are 16x128b pieces of the operand.
+        constexpr int NG = kCW / 4;
+        const int u = (warp - 8) >> 2;               // blocks of 32 tokens u, u + NG, ..
+        const int xcol = quarter * 32;
         bool ok = true;
         for (int c = 0; c < nch && ok; ++c) {
             unsigned char *xs = smem + SM::kX + (c & 1) * SM::kXSlot;
@@ -632,9 +636,9 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if (!wait(&tab_full[c & 1], c >> 1) || !wait(&x_full[c & 1], c >> 1)) break;
             if (partial(c)) {
                 // rows behind the end: zero, so that nothing there (NaN too) enters a product
-                if (!wait(kq_full, c)) break;
+                if (!wait(&k_full[c & 1], c >> 1)) break;
                 const int first = n - (c0 + c) * kTok;
-                for (int i = (warp - 11) * 32 + lane; i < kTok * 8; i += 256) {
+                for (int i = (warp - 8) * 32 + lane; i < kTok * 8; i += 32 * kCW) {
                     const int r = i >> 3, ch = (i & 7) * 16;
                     if (r < first) continue;
 #pragma unroll
@@ -642,7 +646,8 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                         *reinterpret_cast<uint4 *>(xs + x * 16384 + r * 128 + ch) = make_uint4(0, 0, 0, 0);
 #pragma unroll
                     for (int x = 0; x < DK / 64; ++x)
-                        *reinterpret_cast<uint4 *>(smem + SM::kK + x * 16384 + r * 128 + ch) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4 *>(smem + SM::kK + (c & 1) * SM::kKSlot + x * 16384 + r * 128 + ch) =
+                            make_uint4(0, 0, 0, 0);
                 }
                 fence_async_shared();
                 __syncwarp();
@@ -650,63 +655,120 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 if (!wait(fixed, 0)) break;          // every row is zero before any is read
             }
 #pragma unroll 1
-            for (int q = u; q < 4; q += 2, ++wph) {
-                if (wph >= 1 && !(ok = wait(&wx_free[u], wph - 1))) break;
-                const int r = q * 32 + lane;
+            for (int q = u; q < 4; q += NG) {
+                const uint32_t use = 2 * c + (q >> 1);   // of buffer q & 1
+                const uint32_t dst = tmem + lane_base + cW + (q & 1) * 48;
+                if (use >= 1 && !(ok = wait(&wx_free[q & 1], use - 1))) break;
+                tc_fence_after();
                 if (xcol < W) {
-                    const float w = tb[xcol / DV].w[r];
-#pragma unroll 1
-                    for (int e = 0; e < 4; e += 2) {
-                        const uint32_t o0 = swz128(lane * 128 + ((xcol & 63) + 8 * e) * 2), o1 = o0 ^ 16;
-                        const unsigned char *src = xs + (xcol >> 6) * 16384 + q * 4096;
-                        const uint4 x0 = *reinterpret_cast<const uint4 *>(src + o0);
-                        const uint4 x1 = *reinterpret_cast<const uint4 *>(src + o1);
-                        uint4 t[3];
-                        weigh8(x0, w, t[0], t[1], t[2]);
-#pragma unroll
-                        for (int i = 0; i < 3; ++i) *reinterpret_cast<uint4 *>(wx + o0 + i * 8192) = t[i];
-                        weigh8(x1, w, t[0], t[1], t[2]);
-#pragma unroll
-                        for (int i = 0; i < 3; ++i) *reinterpret_cast<uint4 *>(wx + o1 + i * 8192) = t[i];
-                    }
+                    const float2 *wt = reinterpret_cast<const float2 *>(tb[xcol / DV].w + q * 32) + (lane & 3);
+                    const float2 w[4] = {wt[0], wt[4], wt[8], wt[12]};
+                    const uint32_t src =
+                        smem_u32(xs) + (xcol >> 6) * 16384 + swz128((q * 32 + lane) * 128 + (xcol & 63) * 2);
+                    weigh_block(src, dst, w);
                 }
-                fence_async_shared();
+                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&wx_ready[u]);
+                if (lane == 0) mbar_arrive(&wx_ready[q & 1]);
             }
-            if (!ok) break;
-            const float dec = tb[hv].dec;
             __syncwarp();
             if (lane == 0) mbar_arrive(&tab_free[c & 1]);
-            // ---- S <- P(end, start) S + dS
-            if (!wait(ds_full, c)) break;
-            tc_fence_after();
+        }
+    } else if (warp < 4) {
+        // ============================ the state =====================================
+        const int v = quarter * 32 + lane;           // value column (TMEM lane)
+        const bool live = v < W;
+        const int hv = v / DV < HB ? v / DV : 0, vcol = v % DV;
+        const size_t bh = (size_t)(b * p.a.H + h0 + hv);
+        const uint32_t scol = tmem + lane_base + cS;
+        const uint32_t sdst = SM::kS;
+        // 16 state rows of this column at the walk's start
+        auto start = [&](int k, float (&x)[16]) {
 #pragma unroll
-            for (int k = 0; k < NK; k += 16) {
-                float x[16];
-                tmem_ld16(tmem + lane_base + cS + u * NK + k, x);
-                tmem_wait_ld();
+            for (int i = 0; i < 16; ++i) x[i] = 0.f;
+            if (!live) return;
+            if (seg == 0) {
+                if (p.init)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) S[k + i] = fmaf(dec, S[k + i], x[i]);
+                    for (int i = 0; i < 16; ++i) x[i] = p.init[(bh * DK + k + i) * DV + vcol];
+                return;
             }
+            // contributions of the segments before, latest first (segment 0's holds the initial state)
+            float lg = 0.f;
+            for (int g = seg - 1; g >= 0 && lg >= kForgetLog; --g) {
+                const size_t ti = bh * (p.nseg - 1) + g;
+                const float f = ex2(lg), *src = p.tails + (ti * DK + k) * DV + vcol;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = fmaf(f, src[(size_t)i * DV], x[i]);
+                lg += p.decs[ti];
+            }
+        };
+        for (int c = 0; c < nch; ++c) {
+            // ---- the state after chunk c - 1: bf16 copy for R, decayed for chunk c
+            if (c > 0 && (!wait(s_full, c - 1) || !wait(r_done, c - 1))) break;
+            tc_fence_after();
+            if (!wait(&tab_full[c & 1], c >> 1)) break;
+            const float dec = tabs[(c & 1) * 2 + hv].dec;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tab_free[c & 1]);
+#pragma unroll 1
+            for (int k = 0; k < DK; k += 32) {
+                float x[2][16];
+                if (c == 0) {
+                    start(k, x[0]);
+                    start(k + 16, x[1]);
+                } else {
+                    tmem_ld16(scol + k, x[0]);
+                    tmem_ld16(scol + k + 16, x[1]);
+                    tmem_wait_ld();
+                }
+                const uint32_t o = sdst + (k >> 6) * (W * 128) + swz128(v * 128 + (k & 63) * 2);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float *y = x[e >> 1] + 8 * (e & 1);
+                    if (live)
+                        *reinterpret_cast<uint4 *>(smem + (o ^ (16 * e))) = make_uint4(
+                            pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        const float2 y = mul2(make_float2(x[e][i], x[e][i + 1]), make_float2(dec, dec));
+                        x[e][i] = y.x;
+                        x[e][i + 1] = y.y;
+                    }
+                    tmem_st16(scol + k + 16 * e, x[e]);
+                }
+            }
+            tmem_wait_st();
+            fence_async_shared();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(ds_free);
-            if (c + 1 < nch) {
-                if (!wait(r_done, c)) break;         // Q S has read the copy before
-                stage_state();
-            }
+            if (lane == 0) mbar_arrive(s_ready);
         }
-        if (last && live && p.a.state_out && *abort_s == 0) {
+        if (last && p.a.state_out && (nch <= 0 || wait(s_full, nch - 1))) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int k = 0; k < DK; k += 16) {
+                float x[16];
+                if (nch <= 0) {
+                    start(k, x);
+                } else {
+                    tmem_ld16(scol + k, x);
+                    tmem_wait_ld();
+                }
+                if (live)
 #pragma unroll
-            for (int k = 0; k < NK; ++k) p.a.state_out[sidx + (size_t)k * DV] = S[k];
+                    for (int i = 0; i < 16; ++i) p.a.state_out[(bh * DK + k + i) * DV + vcol] = x[i];
+            }
         }
     }
 
     __syncthreads();
     if (*abort_s && tid == 0) {
         // a wait gave up: let copies and MMAs in flight land before shared memory and TMEM go
-        uint64_t *in_flight[] = {&x_full[0], &x_full[1], kq_full, g_full, r_done, ds_full, y_full, kq_free};
+        uint64_t *in_flight[] = {&x_full[0], &x_full[1], &k_full[0], &k_full[1], q_full, g_full, r_done, s_full, y_full};
         for (uint64_t *bar : in_flight) mbar_wait(bar, 0, 64);
     }
     tc_fence_before();
@@ -717,21 +779,28 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 // ---------------------------------------------------------------------------
 // Contributions of the segments to the states after them
 // ---------------------------------------------------------------------------
+constexpr int kTailStages = 3;
+constexpr int kTailThreads = 32 * 19;      // 16 warps of weighted values, loads, MMA issue, weights
+constexpr int kMaxSegChunks = 1024;        // longest segment (its chunks' decays are kept in shared memory)
+
 template <int DK, int W>
 struct TailSmem {
-    static constexpr int kX = 0;                              // v: W/64 blocks
-    static constexpr int kK = kX + (W / 64) * 16384;
-    static constexpr int kWX = kK + (DK / 64) * 16384;        // 3 terms of 128 tokens x 128 columns each
-    static constexpr int kW = kWX + 3 * 32768;                // weights [2][128]
-    static constexpr int kRed = kW + 2 * kTok * 4;            // log-decay sums [2 heads][8 warps]
-    static constexpr int kBar = kRed + 64;
-    static constexpr int kCtl = kBar + 16;
-    static constexpr int kBytes = kCtl + 16;
+    static constexpr int kStage = (W / 64 + DK / 64) * 16384;   // v, then k
+    static constexpr int kW = kTailStages * kStage;              // weights [2][2][128]
+    static constexpr int kSum = kW + 4 * kTok * 4;               // log2 decay of each chunk [2][kMaxSegChunks]
+    static constexpr int kBar = kSum + 2 * kMaxSegChunks * 4;
+    static constexpr int kCtl = kBar + 128;
+    static constexpr int kBytes = kCtl + 32;
+    static_assert(kBytes <= 232448, "shared memory budget");
 };
 
 // grid (nseg - 1, B * nhb): segment g of a head block: tails[g] = the state
 // after it when it starts from zero (segment 0: from the initial state),
-// decs[g] = its log2 decay.  Segments without a successor do nothing.
+// decs[g] = its log2 decay.  Segments without a successor do nothing.  The
+// chunks are taken from the last one back, until what is before has decayed
+// below kForgetLog; every product accumulates onto the state in TMEM, so that
+// the weighted values of one chunk are made while the chunk before is
+// multiplied.  A chunk costs about 1,600 cycles (three products over k).
 template <int DK, int DV, int HB>
 __global__ void __launch_bounds__(kTailThreads, 1)
 tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Params p,
@@ -739,17 +808,27 @@ tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
 {
     constexpr int W = DV * HB;
     using SM = TailSmem<DK, W>;
+    constexpr uint32_t cS = 0, cW = 128;       // TMEM columns: state, two buffers of 4 x 3 x 16
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t sbase = smem_u32(smem);
     if (sbase & 1023u) {
         if (threadIdx.x == 0) atomicAdd(p.err, 1u);
         return;
     }
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + SM::kBar), *done = full + 1;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + SM::kBar);
+    uint64_t *full = bars;             // [3] v and k loaded
+    uint64_t *freed = bars + 3;        // [3] ... and read
+    uint64_t *w_full = bars + 6;       // [2] weights written
+    uint64_t *w_free = bars + 8;       // [2] ... and read
+    uint64_t *wx_ready = bars + 10;    // [2] weighted values written
+    uint64_t *wx_free = bars + 12;     // [2] ... and read
+    uint64_t *done = bars + 14;
     uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + SM::kCtl);
     volatile int *abort_s = reinterpret_cast<volatile int *>(smem + SM::kCtl + 4);
+    float *after_s = reinterpret_cast<float *>(smem + SM::kCtl + 8);     // [2]
+    int *steps_s = reinterpret_cast<int *>(smem + SM::kCtl + 16);
     float *ws = reinterpret_cast<float *>(smem + SM::kW);
-    float *red = reinterpret_cast<float *>(smem + SM::kRed);
+    float *sums = reinterpret_cast<float *>(smem + SM::kSum);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quarter = warp & 3;
     const int b = blockIdx.y / p.nhb, hb = blockIdx.y % p.nhb, h0 = hb * HB, seg = blockIdx.x;
     const int grp = h0 / (p.a.H / p.a.G);
@@ -765,132 +844,193 @@ tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     if (c1 >= nC) return;      // the last segment of its sequence, or behind it: whole chunks only from here
 
     if (tid == 0) {
-        mbar_init(full, 1);
-        mbar_init(done, 1);
+#pragma unroll
+        for (int i = 0; i < 15; ++i) mbar_init(bars + i, i >= 8 && i < 12 ? 16 : 1);
         fence_mbar_init();
         *abort_s = 0;
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
     }
     if (warp == 0) {
-        tmem_alloc(tmem_s, 128);
+        tmem_alloc(tmem_s, 512);
         tmem_relinquish();
+    }
+    // every chunk's log2 decay, and from them how far back the walk goes
+    float A2[HB], bias[HB];
+#pragma unroll
+    for (int h = 0; h < HB; ++h) {
+        A2[h] = p.a.A[h0 + h] * kLog2e;
+        bias[h] = p.a.dt_bias ? p.a.dt_bias[h0 + h] : 0.f;
+    }
+    for (int i = warp; i < p.L; i += kTailThreads / 32) {
+        float s[HB];
+#pragma unroll
+        for (int h = 0; h < HB; ++h) {
+            s[h] = 0.f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float d, la;
+                gate(p, load_dt(p, b, (c0 + i) * kTok + q * 32 + lane, h0 + h) + bias[h], true, A2[h], d, la);
+                s[h] += la;
+            }
+#pragma unroll
+            for (int k = 16; k > 0; k >>= 1) s[h] += __shfl_xor_sync(0xffffffffu, s[h], k);
+            if (lane == 0) sums[h * kMaxSegChunks + i] = s[h];
+        }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_s;
-    auto wait = [&](uint64_t *bar, uint32_t ph) { return wait_phase(bar, ph, abort_s, p.err); };
-    constexpr uint32_t idS = idesc(128, DK, 1, 1, 1);
-    // this thread's token of a chunk, and its head (threads 0-127: the first, 128-255: the second)
-    const int hh = tid >> 7, j = tid & 127;
-    const bool has = hh < HB;
-    const float A2 = has ? p.a.A[h0 + hh] * kLog2e : 0.f;
-    const float bias = has && p.a.dt_bias ? p.a.dt_bias[h0 + hh] : 0.f;
-    float after[HB];           // log2 decay from the end of the chunk to the end of the segment
+    if (tid == 0) {
+        float a[HB];
 #pragma unroll
-    for (int h = 0; h < HB; ++h) after[h] = 0.f;
-    int steps = 0;
-    bool forgot = false;
-    for (int c = c1 - 1; c >= c0; --c) {
-        float d = 0.f, la = 0.f;
-        if (has) gate(p, load_dt(p, b, c * kTok + j, h0 + hh) + bias, true, A2, d, la);   // whole chunks only
-        // once everything is forgotten only the segment's decay is of interest: it is zero as well
-        if (!forgot) {
-            if (tid == 0) {
-                mbar_arrive_expect_tx(full, (W / 64 + DK / 64) * 16384);
+        for (int h = 0; h < HB; ++h) a[h] = 0.f;
+        int k = 0;
+        while (k < p.L && (a[0] >= kForgetLog || a[HB - 1] >= kForgetLog)) {
+            ++k;
+#pragma unroll
+            for (int h = 0; h < HB; ++h) a[h] += sums[h * kMaxSegChunks + p.L - k];
+        }
+        *steps_s = k;
+        after_s[0] = a[0];
+        after_s[1] = a[HB - 1];
+    }
+    __syncthreads();
+    const int steps = *steps_s;
+    auto wait = [&](uint64_t *bar, uint32_t ph) { return wait_phase(bar, ph, abort_s, p.err); };
+
+    if (warp == 16) {
+        if (lane == 0) {
+            for (int i = 0; i < steps; ++i) {
+                const int st = i % kTailStages, t0 = (c1 - 1 - i) * kTok;
+                if (i >= kTailStages && !wait(&freed[st], i / kTailStages - 1)) break;
+                unsigned char *dst = smem + st * SM::kStage;
+                mbar_arrive_expect_tx(&full[st], SM::kStage);
 #pragma unroll
                 for (int x = 0; x < W / 64; ++x)
-                    tma_load_4d(smem + SM::kX + x * 16384, &tm_v, full, h0 * DV + 64 * x, c * kTok, b, 0);
+                    tma_load_4d(dst + x * 16384, &tm_v, &full[st], h0 * DV + 64 * x, t0, b, 0);
 #pragma unroll
                 for (int x = 0; x < DK / 64; ++x)
-                    tma_load_4d(smem + SM::kK + x * 16384, &tm_k, full, grp * DK + 64 * x, c * kTok, b, 0);
+                    tma_load_4d(dst + (W / 64 + x) * 16384, &tm_k, &full[st], grp * DK + 64 * x, t0, b, 0);
             }
         }
-        // suffix sums of the chunk's log-decays
-        float suf = __shfl_down_sync(0xffffffffu, la, 1);
-        if (lane == 31) suf = 0.f;
+        __syncwarp();
+    } else if (warp == 17) {
+        if (elect_one()) {
+            constexpr uint32_t idS = idesc(128, DK, 1, 0, 1);
+            for (int i = 0; i < steps; ++i) {
+                const int st = i % kTailStages;
+                if (!wait(&full[st], i / kTailStages) || !wait(&wx_ready[i & 1], i >> 1)) break;
+                tc_fence_after();
+                const uint64_t dK = sdesc_sw128_mn(sbase + st * SM::kStage + (W / 64) * 16384, 16384);
+                const uint32_t wx = tmem + cW + (i & 1) * 192;
 #pragma unroll
-        for (int s = 1; s < 32; s <<= 1) {
-            const float x = __shfl_down_sync(0xffffffffu, suf, s);
-            if (lane + s < 32) suf += x;
-        }
-        if (lane == 0) red[warp] = suf + la;
-        __syncthreads();
-        float post = hh == 0 ? after[0] : after[HB - 1];
-        for (int q = quarter + 1; q < 4; ++q) post += red[(warp & 4) + q];
-        if (has) ws[tid] = d * ex2(suf + post);
-        forgot = true;
+                for (int s = 0; s < 8; ++s)
 #pragma unroll
-        for (int h = 0; h < HB; ++h) {
-            after[h] += red[4 * h] + red[4 * h + 1] + red[4 * h + 2] + red[4 * h + 3];
-            forgot = forgot && after[h] < kForgetLog;
-        }
-        __syncthreads();
-        wait(full, steps);
-        // weighted values, hi and lo
-        for (int i = tid; i < kTok * (W / 8); i += kTailThreads) {
-            const int r = i & 127, cb = i >> 7;          // token, 8-column chunk
-            const int col = cb * 8;
-            const uint32_t off = (col >> 6) * 16384 + swz128(r * 128 + (col & 63) * 2);
-            const uint4 x = *reinterpret_cast<const uint4 *>(smem + SM::kX + off);
-            const float w = ws[(col / DV) * 128 + r];
-            uint4 t[3];
-            weigh8(x, w, t[0], t[1], t[2]);
-#pragma unroll
-            for (int e = 0; e < 3; ++e) *reinterpret_cast<uint4 *>(smem + SM::kWX + e * 32768 + off) = t[e];
-        }
-        fence_async_shared();
-        __syncthreads();
-        if (*abort_s) break;
-        if (warp == 0 && elect_one()) {
-            tc_fence_after();
-            const uint64_t dK = sdesc_sw128_mn(sbase + SM::kK, 16384), dW = sdesc_sw128_mn(sbase + SM::kWX, 16384);
-#pragma unroll
-            for (int s = 0; s < 8; ++s) {
-                mma_bf16(tmem, dW + s * 128, dK + s * 128, idS, steps + s > 0);
-                mma_bf16(tmem, dW + 2048 + s * 128, dK + s * 128, idS, 1);
-                mma_bf16(tmem, dW + 4096 + s * 128, dK + s * 128, idS, 1);
+                    for (int t = 0; t < 3; ++t)
+                        mma_bf16_ta(tmem + cS, wx + (s >> 1) * 48 + t * 16 + (s & 1) * 8, dK + s * 128, idS,
+                                    i + s + t > 0);
+                mma_commit(&freed[st]);
+                mma_commit(&wx_free[i & 1]);
             }
             mma_commit(done);
         }
-        wait(done, steps);
-        ++steps;
-        __syncthreads();
-        if (*abort_s) break;
-        if (forgot) {
-            // the chunks before it only add to a decay that is zero already
-            break;
-        }
-    }
-    if (!*abort_s) {
-        tc_fence_after();
-        constexpr int NK = DK / 2;
-        const int u = warp >> 2, v = quarter * 32 + lane;
-        const int hv = v / DV < HB ? v / DV : 0, vcol = v % DV;
-        const size_t bh = (size_t)(b * p.a.H + h0 + hv);
-        const float f = HB == 2 && hv == 1 ? ex2(after[HB - 1]) : ex2(after[0]);
-        const bool add = seg == 0 && p.a.state_in && v < W;
-        float *dst = tails + ((bh * (p.nseg - 1) + seg) * DK + u * NK) * DV + vcol;
-        const float *src = p.a.state_in ? p.a.state_in + (bh * DK + u * NK) * DV + vcol : nullptr;
-#pragma unroll 1
-        for (int k = 0; k < NK; k += 16) {
-            float x[16];
-            tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + u * NK + k, x);
-            tmem_wait_ld();
-            if (v < W)
+        __syncwarp();
+    } else if (warp == 18) {
+        // weights: d_j times the decay from token j to the segment's end
+        float post[HB];
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    dst[(size_t)(k + i) * DV] = add ? fmaf(f, src[(size_t)(k + i) * DV], x[i]) : x[i];
+        for (int h = 0; h < HB; ++h) post[h] = 0.f;
+        for (int i = 0; i < steps; ++i) {
+            float d[HB][4], suf[HB][4], la[HB][4];
+#pragma unroll
+            for (int h = 0; h < HB; ++h)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    gate(p, load_dt(p, b, (c1 - 1 - i) * kTok + q * 32 + lane, h0 + h) + bias[h], true, A2[h], d[h][q],
+                         la[h][q]);
+                    suf[h][q] = __shfl_down_sync(0xffffffffu, la[h][q], 1);
+                    if (lane == 31) suf[h][q] = 0.f;
+                }
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1)
+#pragma unroll
+                for (int h = 0; h < HB; ++h)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float x = __shfl_down_sync(0xffffffffu, suf[h][q], s);
+                        if (lane + s < 32) suf[h][q] += x;
+                    }
+            if (i >= 2 && !wait(&w_free[i & 1], (i >> 1) - 1)) break;
+#pragma unroll
+            for (int h = 0; h < HB; ++h)
+#pragma unroll
+                for (int q = 3; q >= 0; --q) {
+                    ws[((i & 1) * 2 + h) * kTok + q * 32 + lane] = d[h][q] * ex2(suf[h][q] + post[h]);
+                    post[h] += __shfl_sync(0xffffffffu, suf[h][q] + la[h][q], 0);
+                }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&w_full[i & 1]);
         }
-        if (tid < HB) decs[(size_t)(b * p.a.H + h0 + tid) * (p.nseg - 1) + seg] = tid == 0 ? after[0] : after[HB - 1];
-    } else if (tid == 0) {
-        mbar_wait(full, 0, 64);
+    } else {
+        // weighted values: token block warp / 4, value columns 32 quarter ..
+        const int q = warp >> 2, xcol = quarter * 32;
+        for (int i = 0; i < steps; ++i) {
+            const int st = i % kTailStages;
+            if (!wait(&w_full[i & 1], i >> 1) || !wait(&full[st], i / kTailStages)) break;
+            float2 w[4] = {};
+            if (xcol < W) {
+                const float2 *wt =
+                    reinterpret_cast<const float2 *>(ws + ((i & 1) * 2 + xcol / DV) * kTok + q * 32) + (lane & 3);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] = wt[4 * k];
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&w_free[i & 1]);
+            if (i >= 2 && !wait(&wx_free[i & 1], (i >> 1) - 1)) break;
+            tc_fence_after();
+            if (xcol < W)
+                weigh_block(sbase + st * SM::kStage + (xcol >> 6) * 16384 +
+                                swz128((q * 32 + lane) * 128 + (xcol & 63) * 2),
+                            tmem + ((uint32_t)(quarter * 32) << 16) + cW + (i & 1) * 192 + q * 48, w);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&wx_ready[i & 1]);
+        }
+        // ---- out: warps 0-7, half of d_k each
+        if (warp < 8 && wait(done, 0)) {
+            tc_fence_after();
+            constexpr int NK = DK / 2;
+            const int u = warp >> 2, v = quarter * 32 + lane;
+            const int hv = v / DV < HB ? v / DV : 0, vcol = v % DV;
+            const size_t bh = (size_t)(b * p.a.H + h0 + hv);
+            const float f = ex2(after_s[hv]);
+            const bool add = seg == 0 && p.a.state_in;
+            float *dst = tails + ((bh * (p.nseg - 1) + seg) * DK + u * NK) * DV + vcol;
+            const float *src = p.a.state_in ? p.a.state_in + (bh * DK + u * NK) * DV + vcol : nullptr;
+#pragma unroll 1
+            for (int k = 0; k < NK; k += 16) {
+                float x[16];
+                tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + cS + u * NK + k, x);
+                tmem_wait_ld();
+                if (v < W)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        dst[(size_t)(k + i) * DV] = add ? fmaf(f, src[(size_t)(k + i) * DV], x[i]) : x[i];
+            }
+        }
+        if (tid < HB) decs[(size_t)(b * p.a.H + h0 + tid) * (p.nseg - 1) + seg] = after_s[tid];
+    }
+    __syncthreads();
+    if (*abort_s && tid == 0) {
+        // a wait gave up: let copies and MMAs in flight land before shared memory and TMEM go
+        for (int i = 0; i < kTailStages; ++i) mbar_wait(&full[i], 0, 64);
         mbar_wait(done, 0, 64);
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) tmem_dealloc(tmem, 128);
+    if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace ssmtc
