@@ -302,6 +302,56 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     const uint32_t tmem = *tmem_s;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
 
+    // The walk's start state, warps 0-15: 32 TMEM lanes (value columns) x DK/4
+    // rows each, every load of a segment's contribution in flight at once.
+    if (warp < 16) {
+        constexpr int NR = DK / 4;
+        const int v = quarter * 32 + lane, r0 = (warp >> 2) * NR;
+        const int hv = v / DV < HB ? v / DV : 0, vcol = v % DV;
+        const size_t bh = (size_t)(b * p.a.H + h0 + hv);
+        float x[NR];
+#pragma unroll
+        for (int i = 0; i < NR; ++i) x[i] = 0.f;
+        if (seg == 0 && p.init && v < W) {
+#pragma unroll
+            for (int i = 0; i < NR; ++i) x[i] = p.init[(bh * DK + r0 + i) * DV + vcol];
+        }
+        // contributions of the segments before, latest first, down to the one
+        // behind which all has decayed (segment 0's holds the initial state)
+        float carry = 0.f;
+        for (int g1 = seg; g1 > 0 && carry >= kForgetLog; g1 -= 32) {
+            const int g = g1 - 1 - lane;
+            const float own = g >= 0 ? p.decs[bh * (p.nseg - 1) + g] : 0.f;
+            float lg = own;                           // decay of this segment and those behind it
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1) {
+                const float y = __shfl_up_sync(0xffffffffu, lg, s);
+                if (lane >= s) lg += y;
+            }
+            const float before = carry + lg - own;    // decay behind this segment
+            const int cnt = __popc(__ballot_sync(0xffffffffu, g >= 0 && (before >= kForgetLog || before == 0.f)));
+            for (int k = 0; k < cnt; ++k) {
+                const float f = ex2(__shfl_sync(0xffffffffu, before, k));
+                const float *src = p.tails + ((bh * (p.nseg - 1) + g1 - 1 - k) * DK + r0) * DV + vcol;
+                if (v < W)
+#pragma unroll
+                    for (int i = 0; i < NR; ++i) x[i] = fmaf(f, src[(size_t)i * DV], x[i]);
+            }
+            carry += __shfl_sync(0xffffffffu, lg, 31);
+        }
+        if (nch > 0) {
+#pragma unroll
+            for (int i = 0; i < NR; i += 16) tmem_st16(tmem + lane_base + cS + r0 + i, x + i);
+            tmem_wait_st();
+        } else if (p.a.state_out && v < W) {          // no tokens: the state passes through
+#pragma unroll
+            for (int i = 0; i < NR; ++i) p.a.state_out[(bh * DK + r0 + i) * DV + vcol] = x[i];
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+
     auto wait = [&](uint64_t *bar, uint32_t ph) { return wait_phase(bar, ph, abort_s, p.err); };
     auto partial = [&](int c) { return (c0 + c + 1) * kTok > n; };          // chunk with tokens behind the end
     // its rows behind the end are other sequences' memory only when n < T
@@ -682,27 +732,6 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         const size_t bh = (size_t)(b * p.a.H + h0 + hv);
         const uint32_t scol = tmem + lane_base + cS;
         const uint32_t sdst = SM::kS;
-        // 16 state rows of this column at the walk's start
-        auto start = [&](int k, float (&x)[16]) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = 0.f;
-            if (!live) return;
-            if (seg == 0) {
-                if (p.init)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] = p.init[(bh * DK + k + i) * DV + vcol];
-                return;
-            }
-            // contributions of the segments before, latest first (segment 0's holds the initial state)
-            float lg = 0.f;
-            for (int g = seg - 1; g >= 0 && lg >= kForgetLog; --g) {
-                const size_t ti = bh * (p.nseg - 1) + g;
-                const float f = ex2(lg), *src = p.tails + (ti * DK + k) * DV + vcol;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = fmaf(f, src[(size_t)i * DV], x[i]);
-                lg += p.decs[ti];
-            }
-        };
         for (int c = 0; c < nch; ++c) {
             // ---- the state after chunk c - 1: bf16 copy for R, decayed for chunk c
             if (c > 0 && (!wait(s_full, c - 1) || !wait(r_done, c - 1))) break;
@@ -714,14 +743,9 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 #pragma unroll 1
             for (int k = 0; k < DK; k += 32) {
                 float x[2][16];
-                if (c == 0) {
-                    start(k, x[0]);
-                    start(k + 16, x[1]);
-                } else {
-                    tmem_ld16(scol + k, x[0]);
-                    tmem_ld16(scol + k + 16, x[1]);
-                    tmem_wait_ld();
-                }
+                tmem_ld16(scol + k, x[0]);
+                tmem_ld16(scol + k + 16, x[1]);
+                tmem_wait_ld();
                 const uint32_t o = sdst + (k >> 6) * (W * 128) + swz128(v * 128 + (k & 63) * 2);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -747,17 +771,13 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             __syncwarp();
             if (lane == 0) mbar_arrive(s_ready);
         }
-        if (last && p.a.state_out && (nch <= 0 || wait(s_full, nch - 1))) {
+        if (last && p.a.state_out && nch > 0 && wait(s_full, nch - 1)) {
             tc_fence_after();
 #pragma unroll 1
             for (int k = 0; k < DK; k += 16) {
                 float x[16];
-                if (nch <= 0) {
-                    start(k, x);
-                } else {
-                    tmem_ld16(scol + k, x);
-                    tmem_wait_ld();
-                }
+                tmem_ld16(scol + k, x);
+                tmem_wait_ld();
                 if (live)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) p.a.state_out[(bh * DK + k + i) * DV + vcol] = x[i];
@@ -780,15 +800,15 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 // Contributions of the segments to the states after them
 // ---------------------------------------------------------------------------
 constexpr int kTailStages = 3;
-constexpr int kTailThreads = 32 * 19;      // 16 warps of weighted values, loads, MMA issue, weights
-constexpr int kMaxSegChunks = 1024;        // longest segment (its chunks' decays are kept in shared memory)
+constexpr int kTailThreads = 32 * 22;      // 16 warps of weighted values, loads, MMA issue, 4 of weights
+constexpr int kMaxSegChunks = 256;         // longest segment (its blocks' decays are kept in shared memory)
 
 template <int DK, int W>
 struct TailSmem {
     static constexpr int kStage = (W / 64 + DK / 64) * 16384;   // v, then k
     static constexpr int kW = kTailStages * kStage;              // weights [2][2][128]
-    static constexpr int kSum = kW + 4 * kTok * 4;               // log2 decay of each chunk [2][kMaxSegChunks]
-    static constexpr int kBar = kSum + 2 * kMaxSegChunks * 4;
+    static constexpr int kSum = kW + 4 * kTok * 4;               // log2 decay of each 32-token block [2][4 kMaxSegChunks]
+    static constexpr int kBar = kSum + 8 * kMaxSegChunks * 4;
     static constexpr int kCtl = kBar + 128;
     static constexpr int kBytes = kCtl + 32;
     static_assert(kBytes <= 232448, "shared memory budget");
@@ -826,7 +846,7 @@ tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + SM::kCtl);
     volatile int *abort_s = reinterpret_cast<volatile int *>(smem + SM::kCtl + 4);
     float *after_s = reinterpret_cast<float *>(smem + SM::kCtl + 8);     // [2]
-    int *steps_s = reinterpret_cast<int *>(smem + SM::kCtl + 16);
+    int *steps_s = reinterpret_cast<int *>(smem + SM::kCtl + 16);         // [2]
     float *ws = reinterpret_cast<float *>(smem + SM::kW);
     float *sums = reinterpret_cast<float *>(smem + SM::kSum);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quarter = warp & 3;
@@ -845,7 +865,7 @@ tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
 
     if (tid == 0) {
 #pragma unroll
-        for (int i = 0; i < 15; ++i) mbar_init(bars + i, i >= 8 && i < 12 ? 16 : 1);
+        for (int i = 0; i < 15; ++i) mbar_init(bars + i, i >= 8 && i < 12 ? 16 : (i == 6 || i == 7 ? 4 : 1));
         fence_mbar_init();
         *abort_s = 0;
         prefetch_tensormap(&tm_k);
@@ -855,49 +875,56 @@ tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         tmem_alloc(tmem_s, 512);
         tmem_relinquish();
     }
-    // every chunk's log2 decay, and from them how far back the walk goes
+    // every 32-token block's log2 decay
     float A2[HB], bias[HB];
 #pragma unroll
     for (int h = 0; h < HB; ++h) {
         A2[h] = p.a.A[h0 + h] * kLog2e;
         bias[h] = p.a.dt_bias ? p.a.dt_bias[h0 + h] : 0.f;
     }
-    for (int i = warp; i < p.L; i += kTailThreads / 32) {
-        float s[HB];
+    const int nb = 4 * p.L;
+    for (int i = warp; i < nb; i += kTailThreads / 32) {
 #pragma unroll
         for (int h = 0; h < HB; ++h) {
-            s[h] = 0.f;
+            float d, s;
+            gate(p, load_dt(p, b, c0 * kTok + i * 32 + lane, h0 + h) + bias[h], true, A2[h], d, s);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float d, la;
-                gate(p, load_dt(p, b, (c0 + i) * kTok + q * 32 + lane, h0 + h) + bias[h], true, A2[h], d, la);
-                s[h] += la;
-            }
-#pragma unroll
-            for (int k = 16; k > 0; k >>= 1) s[h] += __shfl_xor_sync(0xffffffffu, s[h], k);
-            if (lane == 0) sums[h * kMaxSegChunks + i] = s[h];
+            for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+            if (lane == 0) sums[h * 4 * kMaxSegChunks + i] = s;
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_s;
-    if (tid == 0) {
-        float a[HB];
+    // from the last block back: the decay behind each (in place of its own),
+    // and the chunks that are not forgotten at the segment's end
+    if (warp < HB) {
+        float *sum = sums + warp * 4 * kMaxSegChunks, carry = 0.f;
+        int need = 0;
+        for (int i = 0; i < nb; i += 32) {
+            const int blk = nb - 1 - i - lane;
+            const float own = blk >= 0 ? sum[blk] : 0.f;
+            float inc = own;
 #pragma unroll
-        for (int h = 0; h < HB; ++h) a[h] = 0.f;
-        int k = 0;
-        while (k < p.L && (a[0] >= kForgetLog || a[HB - 1] >= kForgetLog)) {
-            ++k;
-#pragma unroll
-            for (int h = 0; h < HB; ++h) a[h] += sums[h * kMaxSegChunks + p.L - k];
+            for (int k = 1; k < 32; k <<= 1) {
+                const float y = __shfl_up_sync(0xffffffffu, inc, k);
+                if (lane >= k) inc += y;
+            }
+            float ex = __shfl_up_sync(0xffffffffu, inc, 1);
+            if (lane == 0) ex = 0.f;
+            if (blk >= 0) sum[blk] = carry + ex;
+            // a chunk counts while what is behind it has not decayed
+            need += __popc(__ballot_sync(0xffffffffu, blk >= 0 && (blk & 3) == 3 && carry + ex >= kForgetLog));
+            carry += __shfl_sync(0xffffffffu, inc, 31);
         }
-        *steps_s = k;
-        after_s[0] = a[0];
-        after_s[1] = a[HB - 1];
+        if (lane == 0) {
+            after_s[warp] = carry;
+            steps_s[warp] = need;
+        }
     }
     __syncthreads();
-    const int steps = *steps_s;
+    const int steps = max(steps_s[0], steps_s[HB - 1]);
     auto wait = [&](uint64_t *bar, uint32_t ph) { return wait_phase(bar, ph, abort_s, p.err); };
 
     if (warp == 16) {
@@ -937,39 +964,37 @@ tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             mma_commit(done);
         }
         __syncwarp();
-    } else if (warp == 18) {
-        // weights: d_j times the decay from token j to the segment's end
-        float post[HB];
+    } else if (warp >= 18) {
+        // weights of token block q: d_j times the decay from token j to the segment's end
+        const int q = warp - 18;
+        float raw[HB];
+        auto fetch = [&](int i) {
 #pragma unroll
-        for (int h = 0; h < HB; ++h) post[h] = 0.f;
+            for (int h = 0; h < HB; ++h) raw[h] = load_dt(p, b, (c1 - 1 - i) * kTok + q * 32 + lane, h0 + h);
+        };
+        if (steps > 0) fetch(0);
         for (int i = 0; i < steps; ++i) {
-            float d[HB][4], suf[HB][4], la[HB][4];
+            float d[HB], suf[HB];
 #pragma unroll
-            for (int h = 0; h < HB; ++h)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    gate(p, load_dt(p, b, (c1 - 1 - i) * kTok + q * 32 + lane, h0 + h) + bias[h], true, A2[h], d[h][q],
-                         la[h][q]);
-                    suf[h][q] = __shfl_down_sync(0xffffffffu, la[h][q], 1);
-                    if (lane == 31) suf[h][q] = 0.f;
-                }
+            for (int h = 0; h < HB; ++h) {
+                float la;
+                gate(p, raw[h] + bias[h], true, A2[h], d[h], la);
+                suf[h] = __shfl_down_sync(0xffffffffu, la, 1);
+                if (lane == 31) suf[h] = 0.f;
+            }
+            if (i + 1 < steps) fetch(i + 1);
 #pragma unroll
             for (int s = 1; s < 32; s <<= 1)
 #pragma unroll
-                for (int h = 0; h < HB; ++h)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float x = __shfl_down_sync(0xffffffffu, suf[h][q], s);
-                        if (lane + s < 32) suf[h][q] += x;
-                    }
+                for (int h = 0; h < HB; ++h) {
+                    const float x = __shfl_down_sync(0xffffffffu, suf[h], s);
+                    if (lane + s < 32) suf[h] += x;
+                }
             if (i >= 2 && !wait(&w_free[i & 1], (i >> 1) - 1)) break;
 #pragma unroll
             for (int h = 0; h < HB; ++h)
-#pragma unroll
-                for (int q = 3; q >= 0; --q) {
-                    ws[((i & 1) * 2 + h) * kTok + q * 32 + lane] = d[h][q] * ex2(suf[h][q] + post[h]);
-                    post[h] += __shfl_sync(0xffffffffu, suf[h][q] + la[h][q], 0);
-                }
+                ws[((i & 1) * 2 + h) * kTok + q * 32 + lane] =
+                    d[h] * ex2(suf[h] + sums[h * 4 * kMaxSegChunks + (p.L - 1 - i) * 4 + q]);
             __syncwarp();
             if (lane == 0) mbar_arrive(&w_full[i & 1]);
         }
