@@ -209,62 +209,79 @@ def vda_scan(q, k, v, alpha_frame, beta, U, *, bidir=False, state=None, state_bw
 # ---------------------------------------------------------------------------
 # Operators around the scan: inputs may be views (last dimension contiguous)
 # ---------------------------------------------------------------------------
-def _view(t, name, dtype=None, shape=None, device=None):
-    """A CUDA tensor whose last dimension is contiguous."""
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor (the library has no CPU path)" % name)
-    if device is not None and t.device != device:
-        raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError("%s must be contiguous in its last dimension" % name)
+# The calls on single tokens are a few microseconds of device time, so what
+# runs on the host before the launch is kept short: each tensor's checks are
+# one expression, spelled out only when it fails.
+def _view(t, name, dtype, shape, device):
+    """`t` is on `device` (a CUDA device), of `dtype` and `shape`, its last
+    dimension contiguous."""
+    if t.device != device or t.dtype is not dtype or t.shape != shape or (t.stride()[-1] != 1 and shape[-1] > 1):
+        _refuse(t, name, dtype, shape, device)
 
 
 def _dense(t, name, dtype, shape, device):
-    _view(t, name, dtype, shape, device)
-    if not t.is_contiguous():
+    if t.device != device or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _refuse(t, name, dtype, shape, device)
         raise ValueError("%s must be contiguous" % name)
+
+
+def _refuse(t, name, dtype, shape, device):
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor (the library has no CPU path)" % name)
+    if t.device != device:
+        raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("%s must be contiguous in its last dimension" % name)
 
 
 def _strides(t, n):
     """Strides of the first n dimensions in elements; a dimension of one entry
     has no stride of its own (torch may report any): its row's width."""
+    st, shape = t.stride(), t.shape
+    if 1 not in shape[:n]:
+        return st[:n]
     w = 1
-    for s in t.shape[n:]:
-        w *= s
-    return tuple(t.stride(i) if t.shape[i] > 1 else w for i in range(n))
+    for d in shape[n:]:
+        w *= d
+    return tuple([st[i] if shape[i] > 1 else w for i in range(n)])
 
 
 def _rows(t, name):
     """The heads of a token are contiguous: [B, T, H, d] with any batch and token stride."""
-    if t.shape[2] > 1 and t.stride(2) != t.shape[3]:
+    if t.shape[2] > 1 and t.stride()[2] != t.shape[3]:
         raise ValueError("%s must have the heads of a token contiguous" % name)
 
 
-def _lengths(lengths, B, device):
-    if lengths is not None:
-        _dense(lengths, "lengths", torch.int32, (B,), device)
+def _cuda(t, name):
+    """The device of the call's first tensor, and its dtype's code."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor (the library has no CPU path)" % name)
+    code = _DT.get(t.dtype)
+    if code is None:
+        raise ValueError("%s must be float32 or bfloat16" % name)
+    return t.device, code
 
 
 def _run(name, device, fn, *args):
-    """Call fn(*args, stream) with `device` current, on its current stream."""
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    """fn(*args, stream) with `device` current, on its current stream."""
+    if device.index == torch._C._cuda_getDevice():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
     else:
         with torch.cuda.device(device):
             st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
-    _raise(name, st)
+    if st != 0:
+        raise _lib.GDNError(name, st)
 
 
-def _result(out, shape, dtype, device, lengths):
+def _result(out, like, shape, lengths):
     """The output: `out`, or a new tensor, zero behind the sequences of a padded batch."""
     if out is None:
-        make = torch.empty if lengths is None else torch.zeros
-        return make(shape, dtype=dtype, device=device)
-    _dense(out, "out", dtype, shape, device)
+        return like.new_empty(shape) if lengths is None else like.new_zeros(shape)
+    _dense(out, "out", like.dtype, shape, like.device)
     return out
 
 
@@ -279,14 +296,12 @@ def short_conv(x, w, bias=None, state=None, *, silu=True, lengths=None, return_s
     each sequence of a padded batch.  Returns (y, last K-1 inputs) (the state
     None if not asked).  A new y is zero behind a sequence's end, a given
     `out` keeps what it held there."""
-    if x.dtype not in _DT:
-        raise ValueError("x must be float32 or bfloat16")
+    dev, code = _cuda(x, "x")
     if x.dim() != 3 or w.dim() != 2:
         raise ValueError("x must be [B, T, C] and w [C, K]")
-    B, T, C = x.shape
+    B, T, C = shape = x.shape
     K = w.shape[1]
-    dev = x.device
-    _view(x, "x")
+    _view(x, "x", x.dtype, shape, dev)
     _dense(w, "w", torch.float32, (C, K), dev)
     if not 2 <= K <= 4:
         raise ValueError("w must have 2 to 4 taps, got %d" % K)
@@ -294,14 +309,19 @@ def short_conv(x, w, bias=None, state=None, *, silu=True, lengths=None, return_s
         _dense(bias, "bias", torch.float32, (C,), dev)
     if state is not None:
         _dense(state, "state", x.dtype, (B, K - 1, C), dev)
-    _lengths(lengths, B, dev)
-    y = _result(out, (B, T, C), x.dtype, dev, lengths)
+    if lengths is not None:
+        _dense(lengths, "lengths", torch.int32, (B,), dev)
+    y = _result(out, x, shape, lengths)
     if state_out is not None:
-        _dense(state_out, "state_out", x.dtype, (B, K - 1, C), dev)
+        if state_out is not state:
+            _dense(state_out, "state_out", x.dtype, (B, K - 1, C), dev)
     elif return_state:
-        state_out = torch.empty((B, K - 1, C), dtype=x.dtype, device=dev)
-    _run("gdn_short_conv", dev, _lib.gdn_short_conv, _ptr(x), *_strides(x, 2), _ptr(w), _ptr(bias), _ptr(state),
-         _ptr(state_out), _ptr(y), _ptr(lengths), B, T, C, K, int(bool(silu)), _DT[x.dtype])
+        state_out = x.new_empty((B, K - 1, C))
+    bs, ts = _strides(x, 2)
+    _run("gdn_short_conv", dev, _lib.load().gdn_short_conv, x.data_ptr(), bs, ts, w.data_ptr(),
+         None if bias is None else bias.data_ptr(), None if state is None else state.data_ptr(),
+         None if state_out is None else state_out.data_ptr(), y.data_ptr(),
+         None if lengths is None else lengths.data_ptr(), B, T, C, K, 1 if silu else 0, code)
     return y, state_out
 
 
@@ -374,39 +394,39 @@ def rotary(q, k, pos, freqs, *, interleaved=False, scale=1.0, q_out=None, k_out=
     interleaved: pairs (2j, 2j+1), else (j, j + rot/2).  q_out / k_out: where
     the results go (q / k itself: in place); new contiguous tensors by default.
     Returns (q', k')."""
-    if q.dtype not in _DT:
-        raise ValueError("q must be float32 or bfloat16")
+    dev, code = _cuda(q, "q")
     if q.dim() != 4 or (k is not None and k.dim() != 4):
         raise ValueError("q and k must be [B, T, heads, d]")
-    B, T, Hq, d = q.shape
-    dev = q.device
-    _view(q, "q")
-    if k is not None:
-        _view(k, "k", q.dtype, (B, T, k.shape[2], d), dev)
-    if pos.dtype not in (torch.int32, torch.int64):
+    B, T, Hq, d = shape = q.shape
+    _view(q, "q", q.dtype, shape, dev)
+    bits = 64 if pos.dtype is torch.int64 else 32 if pos.dtype is torch.int32 else 0
+    if bits == 0:
         raise ValueError("pos must be int32 or int64")
     axes = pos.shape[2] if pos.dim() == 3 else 1
-    _dense(pos, "pos", None, (B, T) if pos.dim() == 2 else (B, T, axes), dev)
+    _dense(pos, "pos", pos.dtype, (B, T, axes) if pos.dim() == 3 else (B, T), dev)
     _dense(freqs, "freqs", torch.int64, (2, freqs.shape[-1]), dev)
     rot = 2 * freqs.shape[1]
     if rot > d:
         raise ValueError("freqs turn %d channels, the heads have %d" % (rot, d))
     if q_out is None:
-        q_out = torch.empty((B, T, Hq, d), dtype=q.dtype, device=dev)
-    else:
-        _view(q_out, "q_out", q.dtype, q.shape, dev)
-    none = (0, 0, 0)
+        q_out = q.new_empty(shape)
+    elif q_out is not q:
+        _view(q_out, "q_out", q.dtype, shape, dev)
+    args = (q.data_ptr(), *_strides(q, 3), q_out.data_ptr(), *_strides(q_out, 3), Hq)
     if k is not None:
+        kshape = (B, T, k.shape[2], d)
+        _view(k, "k", q.dtype, kshape, dev)
         if k_out is None:
-            k_out = torch.empty(tuple(k.shape), dtype=k.dtype, device=dev)
-        else:
-            _view(k_out, "k_out", k.dtype, k.shape, dev)
+            k_out = k.new_empty(kshape)
+        elif k_out is not k:
+            _view(k_out, "k_out", q.dtype, kshape, dev)
+        args += (k.data_ptr(), *_strides(k, 3), k_out.data_ptr(), *_strides(k_out, 3), kshape[2])
     elif k_out is not None:
         raise ValueError("k_out without k")
-    _run("gdn_rotary", dev, _lib.gdn_rotary, _ptr(q), _strides(q, 3), _ptr(q_out), _strides(q_out, 3), Hq, _ptr(k),
-         none if k is None else _strides(k, 3), _ptr(k_out), none if k is None else _strides(k_out, 3),
-         0 if k is None else k.shape[2], _ptr(pos), 64 if pos.dtype == torch.int64 else 32, axes, _ptr(freqs),
-         float(scale), B, T, d, rot, int(bool(interleaved)), _DT[q.dtype])
+    else:
+        args += (None, 0, 0, 0, None, 0, 0, 0, 0)
+    _run("gdn_rotary", dev, _lib.load().gdn_rotary, *args, pos.data_ptr(), bits, axes, freqs.data_ptr(), scale, B, T,
+         d, rot, 1 if interleaved else 0, code)
     return q_out, k_out
 
 
@@ -427,39 +447,51 @@ def ssm_scan(q, k, v, dt, A, D=None, dt_bias=None, state=None, *, softplus=True,
     each sequence of a padded batch.  Returns (o, final state) (the state None
     if not asked), o in q's dtype.  A new o is zero behind a sequence's end, a
     given `out` keeps what it held there."""
-    if q.dtype not in _DT:
-        raise ValueError("q must be float32 or bfloat16")
+    dev, code = _cuda(q, "q")
+    dtype = q.dtype
     if q.dim() != 4 or v.dim() != 4 or dt.dim() != 3:
         raise ValueError("q, k must be [B, T, G, dk], v [B, T, H, dv], dt [B, T, H]")
     B, T, G, dk = q.shape
     H, dv = v.shape[2], v.shape[3]
-    dev = q.device
-    _view(q, "q")
-    _view(k, "k", q.dtype, q.shape, dev)
-    _view(v, "v", q.dtype, (B, T, H, dv), dev)
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        _rows(t, name)
-    if dt.dtype not in (torch.float32, q.dtype):
+    oshape, sshape = (B, T, H, dv), (B, H, dk, dv)
+    _view(q, "q", dtype, q.shape, dev)
+    _view(k, "k", dtype, q.shape, dev)
+    _view(v, "v", dtype, oshape, dev)
+    _rows(q, "q")
+    _rows(k, "k")
+    _rows(v, "v")
+    if dt.dtype is not torch.float32 and dt.dtype is not dtype:
         raise ValueError("dt must be float32 or q's dtype")
-    _view(dt, "dt", None, (B, T, H), dev)
+    _view(dt, "dt", dt.dtype, (B, T, H), dev)
     if G < 1 or H % G:
         raise ValueError("the %d heads of v must be a multiple of the %d groups of q and k" % (H, G))
-    for t, name in ((A, "A"), (D, "D"), (dt_bias, "dt_bias")):
-        if t is not None:
-            _dense(t, name, torch.float32, (H,), dev)
+    _dense(A, "A", torch.float32, (H,), dev)
+    if D is not None:
+        _dense(D, "D", torch.float32, (H,), dev)
+    if dt_bias is not None:
+        _dense(dt_bias, "dt_bias", torch.float32, (H,), dev)
     if state is not None:
-        _dense(state, "state", torch.float32, (B, H, dk, dv), dev)
-    _lengths(lengths, B, dev)
-    o = _result(out, (B, T, H, dv), q.dtype, dev, lengths)
+        _dense(state, "state", torch.float32, sshape, dev)
+    if lengths is not None:
+        _dense(lengths, "lengths", torch.int32, (B,), dev)
+    o = _result(out, q, oshape, lengths)
     if state_out is not None:
-        _dense(state_out, "state_out", torch.float32, (B, H, dk, dv), dev)
+        if state_out is not state:
+            _dense(state_out, "state_out", torch.float32, sshape, dev)
     elif return_state:
-        state_out = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
-    ws, nbytes = _workspace(ssm_workspace_size(B, T, H, G, dk, dv, q.dtype), dev, workspace)
-    _run("gdn_ssm_scan", dev, _lib.gdn_ssm_scan, _ptr(q), _strides(q, 2), _ptr(k), _strides(k, 2), _ptr(v),
-         _strides(v, 2), _ptr(dt), _strides(dt, 2), _ptr(A), _ptr(D), _ptr(dt_bias), _ptr(state), _ptr(state_out),
-         _ptr(o), _ptr(lengths), B, T, H, G, dk, dv, int(bool(softplus)), _DT[q.dtype], _DT[dt.dtype], _ptr(ws),
-         nbytes)
+        state_out = A.new_empty(sshape)
+    lib = _lib.load()
+    nbytes = lib.gdn_ssm_workspace_size(B, T, H, G, dk, dv, code)
+    ws = None
+    if nbytes:
+        ws, nbytes = _workspace(nbytes, dev, workspace)
+        ws = ws.data_ptr()
+    _run("gdn_ssm_scan", dev, lib.gdn_ssm_scan, q.data_ptr(), *_strides(q, 2), k.data_ptr(), *_strides(k, 2),
+         v.data_ptr(), *_strides(v, 2), dt.data_ptr(), *_strides(dt, 2), A.data_ptr(),
+         None if D is None else D.data_ptr(), None if dt_bias is None else dt_bias.data_ptr(),
+         None if state is None else state.data_ptr(), None if state_out is None else state_out.data_ptr(),
+         o.data_ptr(), None if lengths is None else lengths.data_ptr(), B, T, H, G, dk, dv, 1 if softplus else 0, code,
+         _DT[dt.dtype], ws, nbytes)
     return o, state_out
 
 

@@ -743,7 +743,14 @@ gdn_status noalloc_scratch(void **out) {
 namespace gdn {
 PFN_cuTensorMapEncodeTiled_v12000 driver_tensor_map_encoder() { return tensor_map_encoder(); }
 unsigned int *wait_timeout_counter() { return timeout_counter(); }
-int device_sm_count() { return sm_count(); }
+int device_sm_count() {
+    static std::atomic<int> known[64];   // per device; zero: not asked yet
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sm_count();
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) known[dev].store(n = sm_count(), std::memory_order_relaxed);
+    return n;
+}
 }  // namespace gdn
 
 extern "C" {

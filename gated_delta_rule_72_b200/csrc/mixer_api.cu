@@ -117,7 +117,7 @@ gdn_status conv_act(const gdn::conv::Args &a, int B, int silu, cudaStream_t s) {
 template <typename T, int K>
 gdn_status conv_vec(const gdn::conv::Args &a, int B, int silu, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T);
-    const bool vec = a.C % V == 0 && (a.T == 0 || (aligned(a.x, 16) && a.x_ts % V == 0 && a.x_bs % V == 0));
+    const bool vec = a.C % V == 0 && aligned(a.w, 16) && (a.T == 0 || (aligned(a.x, 16) && a.x_ts % V == 0 && a.x_bs % V == 0));
     return vec ? conv_act<T, K, V>(a, B, silu, s) : conv_act<T, K, 1>(a, B, silu, s);
 }
 
@@ -131,12 +131,12 @@ gdn_status conv_width(const gdn::conv::Args &a, int B, int K, int silu, cudaStre
 // ---------------------------------------------------------------------------
 // Rotary positions
 // ---------------------------------------------------------------------------
-template <typename T, int V, bool kInter, bool kElem>
+template <typename T, int V, bool kInter>
 gdn_status launch_rotary(const gdn::rope::Args &a, cudaStream_t s) {
     using namespace gdn::rope;
     const long long blocks = (a.rows + a.tok - 1) / a.tok;
     gdn::LaunchScope ls("rotary", s);
-    rotary_kernel<T, V, kInter, kElem><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+    rotary_kernel<T, V, kInter><<<(unsigned)blocks, kThreads, 0, s>>>(a);
     return launch_status();
 }
 
@@ -151,8 +151,8 @@ gdn_status rotary_type(const gdn::rope::Args &a, int inter, cudaStream_t s) {
             const size_t st[6] = {p->in_bs, p->in_ts, p->in_hs, p->out_bs, p->out_ts, p->out_hs};
             for (size_t x : st) vec = vec && x % V == 0;
         }
-    if (inter) return vec ? launch_rotary<T, V, true, false>(a, s) : launch_rotary<T, 2, true, true>(a, s);
-    return vec ? launch_rotary<T, V, false, false>(a, s) : launch_rotary<T, 1, false, true>(a, s);
+    if (inter) return vec ? launch_rotary<T, V, true>(a, s) : launch_rotary<T, 2, true>(a, s);
+    return vec ? launch_rotary<T, V, false>(a, s) : launch_rotary<T, 1, false>(a, s);
 }
 
 // ---------------------------------------------------------------------------

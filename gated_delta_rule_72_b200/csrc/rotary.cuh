@@ -17,13 +17,14 @@
 // are no multiple of the vector, take the element-wise form.
 #pragma once
 
-#include "common.cuh"
+#include "vecio.cuh"
 
 namespace gdn {
 namespace rope {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTok = 8;        // tokens per block
+constexpr int kUnroll = 4;        // heads in flight a thread
 constexpr int kMaxRot = 256;      // rotated channels of a head
 
 struct Part {
@@ -42,39 +43,47 @@ struct Args {
     bool pos64, copy;              // copy: the channels behind rot are written too
 };
 
+// V elements: one 16-byte access, or element by element (V = 1 or 2).
 template <typename T, int V>
-struct alignas(sizeof(T) * V) Vec { T e[V]; };
-
-// V elements from p: one vector access, or element by element (kElem).
-template <typename T, int V, bool kElem>
-__device__ __forceinline__ void load(const T *p, float (&x)[V]) {
-    if (kElem) {
+struct Io {
+    using Raw = typename Pack<T, V>::Raw;
+    static __device__ __forceinline__ Raw load(const T *p) { return *reinterpret_cast<const Raw *>(p); }
+    static __device__ __forceinline__ void store(T *p, const Raw &r) { *reinterpret_cast<Raw *>(p) = r; }
+    static __device__ __forceinline__ void unpack(const Raw &r, float (&x)[V]) { Pack<T, V>::unpack(r, x); }
+    static __device__ __forceinline__ Raw pack(const float (&x)[V]) { return Pack<T, V>::pack(x); }
+};
+template <typename T>
+struct Io<T, 2> {
+    struct Raw { T a, b; };
+    static __device__ __forceinline__ Raw load(const T *p) { return {p[0], p[1]}; }
+    static __device__ __forceinline__ void store(T *p, const Raw &r) { p[0] = r.a; p[1] = r.b; }
+    static __device__ __forceinline__ void unpack(const Raw &r, float (&x)[2]) { x[0] = to_f32(r.a); x[1] = to_f32(r.b); }
+    static __device__ __forceinline__ Raw pack(const float (&x)[2]) { return {from_f32<T>(x[0]), from_f32<T>(x[1])}; }
+};
+// N (cos, sin) pairs from shared memory.
+template <int N>
+__device__ __forceinline__ void load_cs(const float2 *z, float2 (&c)[N]) {
+    if (N % 2 == 0) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = to_f32(p[i]);
+        for (int i = 0; i + 1 < N; i += 2) {
+            const float4 f = *reinterpret_cast<const float4 *>(z + i);
+            c[i] = make_float2(f.x, f.y);
+            c[i + 1] = make_float2(f.z, f.w);
+        }
     } else {
-        const Vec<T, V> v = *reinterpret_cast<const Vec<T, V> *>(p);
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = to_f32(v.e[i]);
+        for (int i = 0; i < N; ++i) c[i] = z[i];
     }
 }
-template <typename T, int V, bool kElem>
-__device__ __forceinline__ void store(T *p, const float (&x)[V]) {
-    Vec<T, V> v;
-#pragma unroll
-    for (int i = 0; i < V; ++i) v.e[i] = from_f32<T>(x[i]);
-    if (kElem) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) p[i] = v.e[i];
-    } else {
-        *reinterpret_cast<Vec<T, V> *>(p) = v;
-    }
-}
 
-template <typename T, int V, bool kInter, bool kElem>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, int V, bool kInter>
+__global__ void __launch_bounds__(kThreads, 3)
 rotary_kernel(const Args a)
 {
-    __shared__ float2 cs[kMaxTok * kMaxRot / 2];
+    using IO = Io<T, V>;
+    using Raw = typename IO::Raw;
+    constexpr bool kElem = V <= 2;
+    __shared__ __align__(16) float2 cs[kMaxTok * kMaxRot / 2];
     const int pairs = a.rot / 2;
     const long long row0 = (long long)blockIdx.x * a.tok;
     const int nt = (int)min((long long)a.tok, a.rows - row0);
@@ -95,55 +104,96 @@ rotary_kernel(const Args a)
     __syncthreads();
 
     // groups of a head: rotated ones (halves: V channels and their partners),
-    // then the channels behind rot
+    // then the channels behind rot.  A thread keeps its group and strides over
+    // the (token, head) pairs, kUnroll of them in flight.
     const int ng = kInter ? a.rot / V : pairs / V;
     const int nv = ng + (a.copy ? (a.d - a.rot + V - 1) / V : 0);
     const int heads = a.q.heads + a.k.heads;
-    const int items = nt * heads * nv;
-    for (int it = threadIdx.x; it < items; it += kThreads) {
-        const int th = it / nv, g = it - th * nv;
-        const int t = th / heads;
-        int h = th - t * heads;
-        const bool isq = h < a.q.heads;
-        if (!isq) h -= a.q.heads;
-        const Part &P = isq ? a.q : a.k;
-        const long long row = row0 + t;
-        const long long b = row / a.T, tt = row - b * a.T;
-        const T *in = static_cast<const T *>(P.in) + b * P.in_bs + tt * P.in_ts + h * P.in_hs;
-        T *out = static_cast<T *>(P.out) + b * P.out_bs + tt * P.out_ts + h * P.out_hs;
-        if (g >= ng) {
-            const int e = a.rot + (g - ng) * V;
-            if (kElem) {
-                for (int i = e; i < min(e + V, a.d); ++i) out[i] = in[i];
-            } else {
-                float x[V];
-                load<T, V, kElem>(in + e, x);
-                store<T, V, kElem>(out + e, x);
-            }
-        } else if (kInter) {
-            float x[V];
-            load<T, V, kElem>(in + g * V, x);
+    const int slots = nv < kThreads ? kThreads / nv : 1;
+    const int slot = threadIdx.x / nv;
+    if (slot >= slots) return;
+    for (int g = threadIdx.x - slot * nv; g < nv; g += kThreads) {       // (one, unless nv > kThreads)
+        const int total = nt * heads;
+        int t = slot / heads, h = slot - t * heads;
+        for (int it = slot; it < total; it += slots * kUnroll) {
+            const T *in[kUnroll];
+            T *out[kUnroll];
+            int tk[kUnroll];
+            Raw x0[kUnroll], x1[kUnroll];
 #pragma unroll
-            for (int i = 0; i < V; i += 2) {
-                const float2 z = cs[t * pairs + (g * V + i) / 2];
-                const float x0 = x[i], x1 = x[i + 1];
-                x[i] = fmaf(x0, z.x, -x1 * z.y);
-                x[i + 1] = fmaf(x0, z.y, x1 * z.x);
+            for (int u = 0; u < kUnroll; ++u) {
+                in[u] = nullptr;
+                if (it + u * slots < total) {
+                    const bool isq = h < a.q.heads;
+                    const Part &P = isq ? a.q : a.k;
+                    const int hh = isq ? h : h - a.q.heads;
+                    const long long row = row0 + t;
+                    const long long b = a.rows == a.T ? 0 : row / a.T, tt = row - b * a.T;
+                    in[u] = static_cast<const T *>(P.in) + b * P.in_bs + tt * P.in_ts + hh * P.in_hs;
+                    out[u] = static_cast<T *>(P.out) + b * P.out_bs + tt * P.out_ts + hh * P.out_hs;
+                    tk[u] = t;
+                }
+                h += slots;
+                while (h >= heads) {
+                    h -= heads;
+                    ++t;
+                }
             }
-            store<T, V, kElem>(out + g * V, x);
-        } else {
-            float x0[V], x1[V];
-            load<T, V, kElem>(in + g * V, x0);
-            load<T, V, kElem>(in + pairs + g * V, x1);
+            if (g >= ng) {
+                const int e = a.rot + (g - ng) * V;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float2 z = cs[t * pairs + g * V + i];
-                const float u = x0[i], w = x1[i];
-                x0[i] = fmaf(u, z.x, -w * z.y);
-                x1[i] = fmaf(u, z.y, w * z.x);
+                for (int u = 0; u < kUnroll; ++u) {
+                    if (!in[u]) continue;
+                    if (kElem) {
+                        for (int i = e; i < min(e + V, a.d); ++i) out[u][i] = in[u][i];
+                    } else {
+                        x0[u] = IO::load(in[u] + e);
+                    }
+                }
+                if (!kElem)
+#pragma unroll
+                    for (int u = 0; u < kUnroll; ++u)
+                        if (in[u]) IO::store(out[u] + e, x0[u]);
+                continue;
             }
-            store<T, V, kElem>(out + g * V, x0);
-            store<T, V, kElem>(out + pairs + g * V, x1);
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (in[u]) {
+                    x0[u] = IO::load(in[u] + g * V);
+                    if (!kInter) x1[u] = IO::load(in[u] + pairs + g * V);
+                }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                if (!in[u]) continue;
+                if (kInter) {
+                    float2 c[(V + 1) / 2];
+                    float y[V];
+                    load_cs(cs + tk[u] * pairs + g * V / 2, c);
+                    IO::unpack(x0[u], y);
+#pragma unroll
+                    for (int i = 0; i + 1 < V; i += 2) {
+                        const float y0 = y[i], y1 = y[i + 1];
+                        y[i] = fmaf(y0, c[i / 2].x, -y1 * c[i / 2].y);
+                        y[i + 1] = fmaf(y0, c[i / 2].y, y1 * c[i / 2].x);
+                    }
+                    x0[u] = IO::pack(y);
+                } else {
+                    float2 c[V];
+                    float y[V], z[V];
+                    load_cs(cs + tk[u] * pairs + g * V, c);
+                    IO::unpack(x0[u], y);
+                    IO::unpack(x1[u], z);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float y0 = y[i], y1 = z[i];
+                        y[i] = fmaf(y0, c[i].x, -y1 * c[i].y);
+                        z[i] = fmaf(y0, c[i].y, y1 * c[i].x);
+                    }
+                    x0[u] = IO::pack(y);
+                    IO::store(out[u] + pairs + g * V, IO::pack(z));
+                }
+                IO::store(out[u] + g * V, x0[u]);
+            }
         }
     }
 }

@@ -8,27 +8,24 @@
 // and one silu per element stay below that (two special-function operations
 // an element, 16 per SM and cycle, are 0.7 of the time of the bytes at bf16).
 // A thread owns V consecutive channels (16 bytes) for a tile of tokens: the
-// filter and the last K-1 inputs stay in registers, and kBatch rows are
-// loaded before the first is used, so that a thread has kBatch independent
-// 16-byte loads in flight.  A tile re-reads the K-1 rows before it.  Rows or
-// bases that are not 16-byte aligned, and channel counts that are no multiple
-// of V, take the V = 1 form.
+// filter and the K-1 inputs before stay in registers, and a row
+// is loaded kBatch rows before it is used, so that a thread has kBatch
+// independent 16-byte loads in flight all the time.  A tile re-reads the K-1
+// rows before it.  Rows or bases that are not 16-byte aligned, and channel
+// counts that are no multiple of V, take the V = 1 form.
 //
 // The state out is written by the threads of the first tile, which are also
 // the only readers of the state in: each thread has read its channels' state
 // before it writes them, so the state may be updated in place.
 #pragma once
 
-#include "common.cuh"
+#include "vecio.cuh"
 
 namespace gdn {
 namespace conv {
 
 constexpr int kThreads = 128;
 constexpr int kBatch = 8;      // rows loaded ahead
-
-template <typename T, int V>
-struct alignas(sizeof(T) * V) Vec { T e[V]; };
 
 struct Args {
     const void *x;
@@ -44,10 +41,11 @@ struct Args {
 __device__ __forceinline__ float silu(float y) { return __fdividef(y, 1.f + __expf(-y)); }
 
 template <typename T, int K, int V, bool kSilu>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 conv_kernel(const Args a)
 {
-    using Row = Vec<T, V>;
+    using P = Pack<T, V>;
+    using Row = typename P::Raw;
     const int c = (blockIdx.x * kThreads + threadIdx.x) * V;
     if (c >= a.C) return;
     const int b = blockIdx.z;
@@ -59,12 +57,29 @@ conv_kernel(const Args a)
     T *y = static_cast<T *>(a.y) + (size_t)b * a.T * a.C + c;
 
     float w[K][V], bias[V];
+    if (V % 4 == 0) {
+        // V filters of K taps: V K consecutive floats
+        float f[V * K];
+        const float4 *wp = reinterpret_cast<const float4 *>(a.w + (size_t)c * K);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+        for (int i = 0; i < V * K / 4; ++i) *reinterpret_cast<float4 *>(f + 4 * i) = wp[i];
 #pragma unroll
-        for (int j = 0; j < K; ++j) w[j][i] = a.w[(size_t)(c + i) * K + j];
-        bias[i] = a.bias ? a.bias[c + i] : 0.f;
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < K; ++j) w[j][i] = f[i * K + j];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < K; ++j) w[j][i] = a.w[(size_t)(c + i) * K + j];
     }
+#pragma unroll
+    for (int i = 0; i < V; ++i) bias[i] = a.bias ? a.bias[c + i] : 0.f;
+    const int t1 = min(n, t0 + a.tile);
+    Row r[kBatch];
+#pragma unroll
+    for (int m = 0; m < kBatch; ++m)
+        if (t0 + m < t1) r[m] = *reinterpret_cast<const Row *>(x + (size_t)(t0 + m) * a.x_ts);
     // the K-1 rows before the tile, oldest first
     float h[K - 1][V];
     if (t0 == 0) {
@@ -72,14 +87,11 @@ conv_kernel(const Args a)
         const T *si = static_cast<const T *>(a.state_in);
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) s[j].e[i] = from_f32<T>(0.f);
+            s[j] = P::zero();
             if (si) s[j] = *reinterpret_cast<const Row *>(si + ((size_t)b * (K - 1) + j) * a.C + c);
         }
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j)
-#pragma unroll
-            for (int i = 0; i < V; ++i) h[j][i] = to_f32(s[j].e[i]);
+        for (int j = 0; j < K - 1; ++j) P::unpack(s[j], h[j]);
         if (a.state_out) {
             T *so = static_cast<T *>(a.state_out);
 #pragma unroll
@@ -101,35 +113,29 @@ conv_kernel(const Args a)
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) {
             const int p = t0 - (K - 1) + j;   // tiles are longer than K-1 rows
-            const Row r = *reinterpret_cast<const Row *>(x + (size_t)p * a.x_ts);
-#pragma unroll
-            for (int i = 0; i < V; ++i) h[j][i] = to_f32(r.e[i]);
+            P::unpack(*reinterpret_cast<const Row *>(x + (size_t)p * a.x_ts), h[j]);
         }
     }
 
-    const int t1 = min(n, t0 + a.tile);
     for (int t = t0; t < t1; t += kBatch) {
-        Row r[kBatch];
-#pragma unroll
-        for (int m = 0; m < kBatch; ++m)
-            if (t + m < t1) r[m] = *reinterpret_cast<const Row *>(x + (size_t)(t + m) * a.x_ts);
 #pragma unroll
         for (int m = 0; m < kBatch; ++m) {
             if (t + m >= t1) break;
-            Row out;
+            float xi[V], out[V];
+            P::unpack(r[m], xi);
+            if (t + m + kBatch < t1) r[m] = *reinterpret_cast<const Row *>(x + (size_t)(t + m + kBatch) * a.x_ts);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float xi = to_f32(r[m].e[i]);
                 float acc = bias[i];
 #pragma unroll
                 for (int j = 0; j < K - 1; ++j) acc = fmaf(w[j][i], h[j][i], acc);
-                acc = fmaf(w[K - 1][i], xi, acc);
+                acc = fmaf(w[K - 1][i], xi[i], acc);
 #pragma unroll
                 for (int j = 0; j + 1 < K - 1; ++j) h[j][i] = h[j + 1][i];
-                h[K - 2][i] = xi;
-                out.e[i] = from_f32<T>(kSilu ? silu(acc) : acc);
+                h[K - 2][i] = xi[i];
+                out[i] = kSilu ? silu(acc) : acc;
             }
-            *reinterpret_cast<Row *>(y + (size_t)(t + m) * a.C) = out;
+            *reinterpret_cast<Row *>(y + (size_t)(t + m) * a.C) = P::pack(out);
         }
     }
 }
