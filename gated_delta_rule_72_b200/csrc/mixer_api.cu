@@ -94,18 +94,18 @@ constexpr int kMaxTokens = 1 << 30;
 template <typename T, int K, int V, bool kSilu>
 gdn_status launch_conv(gdn::conv::Args a, int B, cudaStream_t s) {
     using namespace gdn::conv;
-    const int cx = (a.C + kThreads * V - 1) / (kThreads * V);
-    // long tiles re-read fewer rows before them; shorter ones when a call
-    // would not fill the GPU with four blocks an SM
-    const long long want = 4ll * gdn::device_sm_count();
-    int tile = 64;
-    while (tile > kBatch && (long long)cx * B * ((a.T + tile - 1) / tile) < want) tile /= 2;
-    const int least = (a.T + 65534) / 65535;               // grid.y limit
-    if (tile < least) tile = (least + kBatch - 1) / kBatch * kBatch;
-    a.tile = tile;
-    const int ty = a.T > 0 ? (a.T + tile - 1) / tile : 1;
+    // One wave of threads (kBlocks blocks an SM), each with one tile of tokens:
+    // the longest tiles that fill the GPU re-read the fewest rows.
+    const long long groups = ((long long)a.C + V - 1) / V * B;
+    const long long threads = (long long)gdn::device_sm_count() * kBlocks<V> * kThreads;
+    long long tile = (groups * a.T + threads - 1) / threads;
+    tile = (tile + kBatch - 1) / kBatch * kBatch;
+    if (tile < kBatch) tile = kBatch;
+    a.tile = (int)tile;
+    a.ntile = a.T > 0 ? (int)((a.T + tile - 1) / tile) : 1;
+    const long long blocks = (groups * a.ntile + kThreads - 1) / kThreads;
     gdn::LaunchScope ls("short_conv", s);
-    conv_kernel<T, K, V, kSilu><<<dim3(cx, ty, B), kThreads, 0, s>>>(a);
+    conv_kernel<T, K, V, kSilu><<<(unsigned)blocks, kThreads, 0, s>>>(a);
     return launch_status();
 }
 
@@ -132,9 +132,16 @@ gdn_status conv_width(const gdn::conv::Args &a, int B, int K, int silu, cudaStre
 // Rotary positions
 // ---------------------------------------------------------------------------
 template <typename T, int V, bool kInter>
-gdn_status launch_rotary(const gdn::rope::Args &a, cudaStream_t s) {
+gdn_status launch_rotary(gdn::rope::Args a, cudaStream_t s) {
     using namespace gdn::rope;
-    const long long blocks = (a.rows + a.tok - 1) / a.tok;
+    const int nv = rotated_groups(a.rot, V, kInter) + (a.copy ? copied_groups(a.d - a.rot, V, kInter) : 0);
+    // split the heads of a token over as many threads as leave four blocks an SM
+    const int heads = a.q.heads > a.k.heads ? a.q.heads : a.k.heads;
+    const long long want = 4ll * gdn::device_sm_count() * kThreads;
+    long long split = want / (a.rows * nv);
+    a.hsplit = (int)(split < 1 ? 1 : (split > heads ? heads : split));
+    const long long blocks = (a.rows * nv * a.hsplit + kThreads - 1) / kThreads;
+    if (blocks > 0x7fffffffll) return GDN_ERR_SHAPE;
     gdn::LaunchScope ls("rotary", s);
     rotary_kernel<T, V, kInter><<<(unsigned)blocks, kThreads, 0, s>>>(a);
     return launch_status();
@@ -143,7 +150,7 @@ gdn_status launch_rotary(const gdn::rope::Args &a, cudaStream_t s) {
 template <typename T>
 gdn_status rotary_type(const gdn::rope::Args &a, int inter, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T);
-    bool vec = a.rot % V == 0 && (inter || (a.rot / 2) % V == 0) && (!a.copy || (a.d - a.rot) % V == 0);
+    bool vec = a.rot % V == 0 && (inter || (a.rot / 2) % V == 0) && (!a.copy || (a.d - a.rot) % (inter ? V : 2 * V) == 0);
     const gdn::rope::Part *ps[2] = {&a.q, &a.k};
     for (const gdn::rope::Part *p : ps)
         if (p->heads) {
@@ -328,7 +335,7 @@ gdn_status gdn_short_conv(const void *x, size_t x_batch_stride, size_t x_token_s
     if (overlap(y, ny, x, nx) || overlap(y, ny, state_in, ns) || overlap(y, ny, state_out, ns) ||
         overlap(state_out, ns, x, nx) || (overlap(state_out, ns, state_in, ns) && state_out != state_in))
         return GDN_ERR_SHAPE;
-    const gdn::conv::Args a{x, x_batch_stride, x_token_stride, w, bias, state_in, state_out, y, lengths, T, C, 0};
+    const gdn::conv::Args a{x, x_batch_stride, x_token_stride, w, bias, state_in, state_out, y, lengths, B, T, C, 0, 0};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return dt == GDN_F32 ? conv_width<float>(a, B, K, silu, s) : conv_width<bf16>(a, B, K, silu, s);
 }
@@ -378,16 +385,13 @@ gdn_status gdn_rotary(const void *q, size_t q_batch_stride, size_t q_token_strid
     a.pos = pos;
     a.freqs = static_cast<const long long *>(freqs);
     a.scale = scale;
-    a.rows = (long long)B * T;
     a.T = T;
     a.d = d;
     a.rot = rot;
     a.axes = axes;
     a.pos64 = pos_bits == 64;
     a.copy = copy;
-    // as many tokens a block as leave eight blocks an SM
-    const long long tok = a.rows / (8ll * gdn::device_sm_count());
-    a.tok = (int)(tok < 1 ? 1 : (tok > gdn::rope::kMaxTok ? gdn::rope::kMaxTok : tok));
+    a.rows = (long long)B * T;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return dt == GDN_F32 ? rotary_type<float>(a, interleaved, s) : rotary_type<bf16>(a, interleaved, s);
 }

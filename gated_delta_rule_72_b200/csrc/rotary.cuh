@@ -10,11 +10,12 @@
 // billion costs no accuracy (fp32 angles are off by 0.06 rad at a million).
 // The top 32 bits, as a signed fraction of a turn, give cos and sin.
 //
-// HBM-bound: q and k are read once and written once.  A block takes `tok`
-// tokens: it makes the tokens' cos and sin once in shared memory (they serve
-// every head of q and k), then its threads stride over (token, head, vector)
-// with 16-byte accesses.  Rows that are not 16-byte aligned, and sizes that
-// are no multiple of the vector, take the element-wise form.
+// HBM-bound: q and k are read once and written once.  A thread keeps one group
+// of channels of one token: it makes the group's cos and sin once, in
+// registers, and turns that group of every head of q and k (few tokens: of
+// every hsplit-th head), kUnroll 16-byte loads in flight and no barrier.  Rows
+// that are not 16-byte aligned, and sizes that are no multiple of the vector,
+// take the element-wise form.
 #pragma once
 
 #include "vecio.cuh"
@@ -23,7 +24,6 @@ namespace gdn {
 namespace rope {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTok = 8;        // tokens per block
 constexpr int kUnroll = 4;        // heads in flight a thread
 constexpr int kMaxRot = 256;      // rotated channels of a head
 
@@ -39,7 +39,7 @@ struct Args {
     const long long *freqs;        // [2, rot/2]: phase per position, axis
     float scale;
     long long rows;                // B * T
-    int T, d, rot, axes, tok;
+    int T, d, rot, axes, hsplit;
     bool pos64, copy;              // copy: the channels behind rot are written too
 };
 
@@ -60,38 +60,112 @@ struct Io<T, 2> {
     static __device__ __forceinline__ void unpack(const Raw &r, float (&x)[2]) { x[0] = to_f32(r.a); x[1] = to_f32(r.b); }
     static __device__ __forceinline__ Raw pack(const float (&x)[2]) { return {from_f32<T>(x[0]), from_f32<T>(x[1])}; }
 };
-// N (cos, sin) pairs from shared memory.
-template <int N>
-__device__ __forceinline__ void load_cs(const float2 *z, float2 (&c)[N]) {
-    if (N % 2 == 0) {
-#pragma unroll
-        for (int i = 0; i + 1 < N; i += 2) {
-            const float4 f = *reinterpret_cast<const float4 *>(z + i);
-            c[i] = make_float2(f.x, f.y);
-            c[i + 1] = make_float2(f.z, f.w);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) c[i] = z[i];
-    }
-}
-
-template <typename T, int V, bool kInter>
-__global__ void __launch_bounds__(kThreads, 3)
-rotary_kernel(const Args a)
+// Every hsplit-th head of one tensor (q or k) from h0 on: in, out at this
+// thread's token and channels, cs the group's (cos, sin).  Halves: the second
+// V channels stand `off` behind the first (two: they exist).  A group behind
+// rot is copied by the same accesses, so that a warp of both kinds does not
+// take two paths.
+template <typename T, int V, bool kInter, int N>
+__device__ __forceinline__ void turn_heads(const T *in, T *out, size_t in_hs, size_t out_hs, int h0, int hsplit,
+                                           int heads, int off, bool two, bool behind, const float2 (&cs)[N])
 {
     using IO = Io<T, V>;
     using Raw = typename IO::Raw;
-    constexpr bool kElem = V <= 2;
-    __shared__ __align__(16) float2 cs[kMaxTok * kMaxRot / 2];
+    in += h0 * in_hs;
+    out += h0 * out_hs;
+    in_hs *= hsplit;
+    out_hs *= hsplit;
+    for (int h = h0; h < heads; h += hsplit * kUnroll) {
+        Raw x0[kUnroll], x1[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            if (h + u * hsplit < heads) {
+                x0[u] = IO::load(in + u * in_hs);
+                if (!kInter && two) x1[u] = IO::load(in + u * in_hs + off);
+            }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            if (h + u * hsplit >= heads) break;
+            if (!behind) {
+                float y[V], w[V];
+                IO::unpack(x0[u], y);
+                if (kInter) {
+#pragma unroll
+                    for (int i = 0; i + 1 < V; i += 2) {
+                        const float y0 = y[i], y1 = y[i + 1];
+                        y[i] = fmaf(y0, cs[i / 2].x, -y1 * cs[i / 2].y);
+                        y[i + 1] = fmaf(y0, cs[i / 2].y, y1 * cs[i / 2].x);
+                    }
+                } else {
+                    IO::unpack(x1[u], w);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float y0 = y[i], y1 = w[i];
+                        y[i] = fmaf(y0, cs[i].x, -y1 * cs[i].y);
+                        w[i] = fmaf(y0, cs[i].y, y1 * cs[i].x);
+                    }
+                    x1[u] = IO::pack(w);
+                }
+                x0[u] = IO::pack(y);
+            }
+            IO::store(out + u * out_hs, x0[u]);
+            if (!kInter && two) IO::store(out + u * out_hs + off, x1[u]);
+        }
+        in += kUnroll * in_hs;
+        out += kUnroll * out_hs;
+    }
+}
+
+// Groups of V channels (halves: twice V) of a head of d channels.
+__host__ __device__ __forceinline__ int rotated_groups(int rot, int V, bool inter) {
+    return inter ? rot / V : rot / 2 / V;
+}
+__host__ __device__ __forceinline__ int copied_groups(int rest, int V, bool inter) {
+    const int w = inter ? V : 2 * V;
+    return (rest + w - 1) / w;
+}
+
+// Threads: groups of channels fastest, then head splits, then tokens.
+template <typename T, int V, bool kInter>
+__global__ void __launch_bounds__(kThreads)
+rotary_kernel(const Args a)
+{
+    constexpr int N = kInter ? (V + 1) / 2 : V;       // pairs of a group
     const int pairs = a.rot / 2;
-    const long long row0 = (long long)blockIdx.x * a.tok;
-    const int nt = (int)min((long long)a.tok, a.rows - row0);
-    for (int i = threadIdx.x; i < nt * pairs; i += kThreads) {
-        const int t = i / pairs, j = i - t * pairs;
-        long long ax = a.freqs[pairs + j];
-        ax = ax < 0 ? 0 : (ax >= a.axes ? a.axes - 1 : ax);
-        const size_t pi = (size_t)(row0 + t) * a.axes + (size_t)ax;
+    const int ng = rotated_groups(a.rot, V, kInter);
+    const int nc = a.copy ? copied_groups(a.d - a.rot, V, kInter) : 0, nv = ng + nc;
+    const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
+    const int per = nv * a.hsplit;
+    const long long row = id / per;
+    if (row >= a.rows) return;
+    const int rest = (int)(id - row * per), h0 = rest / nv, g = rest - h0 * nv;
+    const long long b = row / a.T, t = row - b * a.T;
+    const bool behind = g >= ng;
+    const int e = behind ? a.rot + (g - ng) * V : g * V;
+    const T *qi = static_cast<const T *>(a.q.in) + b * a.q.in_bs + t * a.q.in_ts + e;
+    T *qo = static_cast<T *>(a.q.out) + b * a.q.out_bs + t * a.q.out_ts + e;
+    const T *ki = static_cast<const T *>(a.k.in) + b * a.k.in_bs + t * a.k.in_ts + e;
+    T *ko = static_cast<T *>(a.k.out) + b * a.k.out_bs + t * a.k.out_ts + e;
+    // the second half of a group (halves); V = 1, 2 groups may end inside d
+    const int off = behind ? nc * V : pairs;
+    const bool two = !kInter && e + off < a.d;
+    if (kInter && V == 2 && behind && e + 1 >= a.d) {      // the last channel of an odd rest
+        for (int h = h0; h < a.q.heads; h += a.hsplit) qo[h * a.q.out_hs] = qi[h * a.q.in_hs];
+        for (int h = h0; h < a.k.heads; h += a.hsplit) ko[h * a.k.out_hs] = ki[h * a.k.in_hs];
+        return;
+    }
+    float2 cs[N];
+    const int j0 = kInter ? e / 2 : e;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (behind) break;
+        const int j = j0 + i;
+        long long ax = 0;
+        if (a.axes > 1) {
+            ax = a.freqs[pairs + j];
+            ax = ax < 0 ? 0 : (ax >= a.axes ? a.axes - 1 : ax);
+        }
+        const size_t pi = (size_t)row * a.axes + (size_t)ax;
         const long long p = a.pos64 ? static_cast<const long long *>(a.pos)[pi]
                                     : (long long)static_cast<const int *>(a.pos)[pi];
         const unsigned long long ph = (unsigned long long)p * (unsigned long long)a.freqs[j];
@@ -101,101 +175,8 @@ rotary_kernel(const Args a)
         sincospif((float)turn * 0x1p-31f, &s, &c);
         cs[i] = make_float2(c * a.scale, s * a.scale);
     }
-    __syncthreads();
-
-    // groups of a head: rotated ones (halves: V channels and their partners),
-    // then the channels behind rot.  A thread keeps its group and strides over
-    // the (token, head) pairs, kUnroll of them in flight.
-    const int ng = kInter ? a.rot / V : pairs / V;
-    const int nv = ng + (a.copy ? (a.d - a.rot + V - 1) / V : 0);
-    const int heads = a.q.heads + a.k.heads;
-    const int slots = nv < kThreads ? kThreads / nv : 1;
-    const int slot = threadIdx.x / nv;
-    if (slot >= slots) return;
-    for (int g = threadIdx.x - slot * nv; g < nv; g += kThreads) {       // (one, unless nv > kThreads)
-        const int total = nt * heads;
-        int t = slot / heads, h = slot - t * heads;
-        for (int it = slot; it < total; it += slots * kUnroll) {
-            const T *in[kUnroll];
-            T *out[kUnroll];
-            int tk[kUnroll];
-            Raw x0[kUnroll], x1[kUnroll];
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                in[u] = nullptr;
-                if (it + u * slots < total) {
-                    const bool isq = h < a.q.heads;
-                    const Part &P = isq ? a.q : a.k;
-                    const int hh = isq ? h : h - a.q.heads;
-                    const long long row = row0 + t;
-                    const long long b = a.rows == a.T ? 0 : row / a.T, tt = row - b * a.T;
-                    in[u] = static_cast<const T *>(P.in) + b * P.in_bs + tt * P.in_ts + hh * P.in_hs;
-                    out[u] = static_cast<T *>(P.out) + b * P.out_bs + tt * P.out_ts + hh * P.out_hs;
-                    tk[u] = t;
-                }
-                h += slots;
-                while (h >= heads) {
-                    h -= heads;
-                    ++t;
-                }
-            }
-            if (g >= ng) {
-                const int e = a.rot + (g - ng) * V;
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    if (!in[u]) continue;
-                    if (kElem) {
-                        for (int i = e; i < min(e + V, a.d); ++i) out[u][i] = in[u][i];
-                    } else {
-                        x0[u] = IO::load(in[u] + e);
-                    }
-                }
-                if (!kElem)
-#pragma unroll
-                    for (int u = 0; u < kUnroll; ++u)
-                        if (in[u]) IO::store(out[u] + e, x0[u]);
-                continue;
-            }
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u)
-                if (in[u]) {
-                    x0[u] = IO::load(in[u] + g * V);
-                    if (!kInter) x1[u] = IO::load(in[u] + pairs + g * V);
-                }
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                if (!in[u]) continue;
-                if (kInter) {
-                    float2 c[(V + 1) / 2];
-                    float y[V];
-                    load_cs(cs + tk[u] * pairs + g * V / 2, c);
-                    IO::unpack(x0[u], y);
-#pragma unroll
-                    for (int i = 0; i + 1 < V; i += 2) {
-                        const float y0 = y[i], y1 = y[i + 1];
-                        y[i] = fmaf(y0, c[i / 2].x, -y1 * c[i / 2].y);
-                        y[i + 1] = fmaf(y0, c[i / 2].y, y1 * c[i / 2].x);
-                    }
-                    x0[u] = IO::pack(y);
-                } else {
-                    float2 c[V];
-                    float y[V], z[V];
-                    load_cs(cs + tk[u] * pairs + g * V, c);
-                    IO::unpack(x0[u], y);
-                    IO::unpack(x1[u], z);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float y0 = y[i], y1 = z[i];
-                        y[i] = fmaf(y0, c[i].x, -y1 * c[i].y);
-                        z[i] = fmaf(y0, c[i].y, y1 * c[i].x);
-                    }
-                    x0[u] = IO::pack(y);
-                    IO::store(out[u] + pairs + g * V, IO::pack(z));
-                }
-                IO::store(out[u] + g * V, x0[u]);
-            }
-        }
-    }
+    turn_heads<T, V, kInter>(qi, qo, a.q.in_hs, a.q.out_hs, h0, a.hsplit, a.q.heads, off, two, behind, cs);
+    if (a.k.heads) turn_heads<T, V, kInter>(ki, ko, a.k.in_hs, a.k.out_hs, h0, a.hsplit, a.k.heads, off, two, behind, cs);
 }
 
 }  // namespace rope

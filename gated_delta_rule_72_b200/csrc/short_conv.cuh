@@ -25,6 +25,7 @@ namespace gdn {
 namespace conv {
 
 constexpr int kThreads = 128;
+template <int V> constexpr int kBlocks = V == 1 ? 10 : 3;     // per SM
 constexpr int kBatch = 8;      // rows loaded ahead
 
 struct Args {
@@ -35,23 +36,37 @@ struct Args {
     void *state_out;           // [B, K-1, C] or NULL
     void *y;                   // [B, T, C]
     const int *lengths;        // [B] or NULL
-    int T, C, tile;            // tile: tokens per block, a multiple of kBatch
+    int B, T, C, tile, ntile;  // tile: tokens per thread, a multiple of kBatch
 };
 
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c, r;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 r, a, b, c;\n\t"
+        "mov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
 __device__ __forceinline__ float silu(float y) { return __fdividef(y, 1.f + __expf(-y)); }
 
 template <typename T, int K, int V, bool kSilu>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, kBlocks<V>)
 conv_kernel(const Args a)
 {
     using P = Pack<T, V>;
     using Row = typename P::Raw;
-    const int c = (blockIdx.x * kThreads + threadIdx.x) * V;
-    if (c >= a.C) return;
-    const int b = blockIdx.z;
+    // thread -> (sequence, tile, channels), channels fastest
+    const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
+    const int groups = (a.C + V - 1) / V;
+    const long long bt = id / groups;
+    const int b = (int)(bt / a.ntile);
+    if (b >= a.B) return;
+    const int c = (int)(id - bt * groups) * V;
     int n = a.T;
     if (a.lengths) n = min(max(a.lengths[b], 0), a.T);
-    const int t0 = blockIdx.y * a.tile;
+    const int t0 = (int)(bt - (long long)b * a.ntile) * a.tile;
     if (t0 >= n && t0 > 0) return;
     const T *x = static_cast<const T *>(a.x) + (size_t)b * a.x_bs + c;
     T *y = static_cast<T *>(a.y) + (size_t)b * a.T * a.C + c;
@@ -124,16 +139,30 @@ conv_kernel(const Args a)
             float xi[V], out[V];
             P::unpack(r[m], xi);
             if (t + m + kBatch < t1) r[m] = *reinterpret_cast<const Row *>(x + (size_t)(t + m + kBatch) * a.x_ts);
+            // two channels an instruction
+            if (V % 2 == 0) {
+#pragma unroll
+                for (int i = 0; i + 1 < V; i += 2) {
+                    float2 acc = make_float2(bias[i], bias[i + 1]);
+#pragma unroll
+                    for (int j = 0; j < K - 1; ++j)
+                        acc = fma2(make_float2(w[j][i], w[j][i + 1]), make_float2(h[j][i], h[j][i + 1]), acc);
+                    acc = fma2(make_float2(w[K - 1][i], w[K - 1][i + 1]), make_float2(xi[i], xi[i + 1]), acc);
+                    out[i] = acc.x;
+                    out[i + 1] = acc.y;
+                }
+            } else {
+                float acc = bias[0];
+#pragma unroll
+                for (int j = 0; j < K - 1; ++j) acc = fmaf(w[j][0], h[j][0], acc);
+                out[0] = fmaf(w[K - 1][0], xi[0], acc);
+            }
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                float acc = bias[i];
-#pragma unroll
-                for (int j = 0; j < K - 1; ++j) acc = fmaf(w[j][i], h[j][i], acc);
-                acc = fmaf(w[K - 1][i], xi[i], acc);
 #pragma unroll
                 for (int j = 0; j + 1 < K - 1; ++j) h[j][i] = h[j + 1][i];
                 h[K - 2][i] = xi[i];
-                out[i] = kSilu ? silu(acc) : acc;
+                if (kSilu) out[i] = silu(out[i]);
             }
             *reinterpret_cast<Row *>(y + (size_t)(t + m) * a.C) = P::pack(out);
         }
