@@ -11,6 +11,7 @@
 #include "launch_stats.cuh"
 #include "rotary.cuh"
 #include "short_conv.cuh"
+#include "ssm_cols.cuh"
 #include "ssm_tc.cuh"
 #include "ssm_token.cuh"
 
@@ -187,10 +188,35 @@ gdn_status token_cols(const Scan &c) {
     return launch_token<DK, DV, 32, T, Td>(c);
 }
 
+// Several tokens: a warp for every 8 columns, in blocks as large as leave one
+// for every SM (the warps of a block share the staged q and k).
+template <int DK, int DV, typename T, typename Td>
+gdn_status launch_cols(const Scan &c) {
+    using namespace gdn::ssm::cols;
+    const long long all = (long long)c.a.B * c.a.H * (DV / 8);
+    int warps = kMaxWarps;
+    while (warps > 1 && all / warps < gdn::device_sm_count()) warps /= 2;
+    const int smem = smem_bytes<DK, T>(warps);
+    unsigned int *err = gdn::wait_timeout_counter();
+    if (!err) return GDN_ERR_CUDA;
+    auto kern = cols_kernel<DK, DV, T, Td>;
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return GDN_ERR_CUDA;
+    gdn::LaunchScope ls("ssm_cols", c.stream);
+    kern<<<dim3(DV / (8 * warps), c.a.B * c.a.H), 32 * warps, smem, c.stream>>>(c.a, err);
+    return launch_status();
+}
+
+template <int DK, int DV, typename T, typename Td>
+gdn_status token_path(const Scan &c) {
+    return c.a.T == 1 ? token_cols<DK, DV, T, Td>(c) : launch_cols<DK, DV, T, Td>(c);
+}
+
 template <typename T, typename Td>
 gdn_status token_dims(const Scan &c) {
-    if (c.dk == 128) return c.dv == 128 ? token_cols<128, 128, T, Td>(c) : token_cols<128, 64, T, Td>(c);
-    return c.dv == 128 ? token_cols<64, 128, T, Td>(c) : token_cols<64, 64, T, Td>(c);
+    if (c.dk == 128) return c.dv == 128 ? token_path<128, 128, T, Td>(c) : token_path<128, 64, T, Td>(c);
+    return c.dv == 128 ? token_path<64, 128, T, Td>(c) : token_path<64, 64, T, Td>(c);
 }
 
 // ---------------------------------------------------------------------------
