@@ -11,6 +11,7 @@
 #include "launch_stats.cuh"
 #include "rotary.cuh"
 #include "short_conv.cuh"
+#include "ssm_chunk.cuh"
 #include "ssm_cols.cuh"
 #include "ssm_tc.cuh"
 #include "ssm_token.cuh"
@@ -224,12 +225,64 @@ gdn_status token_dims(const Scan &c) {
 // ---------------------------------------------------------------------------
 // Calls of at most this many tokens run token by token.
 constexpr int kTokenCall = 32;
-// Fewest chunks of a segment.
+// Fewest chunks of a segment, and of a walk that is cut: the contributions'
+// launch costs as much as five chunks of a walk.
 constexpr int kMinSegChunks = 2;
+constexpr int kMinSegmented = 6;
 
 bool use_tc(int T, gdn_dtype t) { return t == GDN_BF16 && T > kTokenCall; }
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// ---------------------------------------------------------------------------
+// Chunked path of the scan on the CUDA cores (fp32)
+// ---------------------------------------------------------------------------
+bool use_chunks(int T, gdn_dtype t) { return t == GDN_F32 && T > kTokenCall; }
+
+struct ChunkPlan {
+    int nc;
+    size_t decs, bytes;
+};
+ChunkPlan plan_chunks(int B, int T, int H, int dk, int dv) {
+    ChunkPlan p{};
+    p.nc = (T + gdn::ssm::chunk::kTok - 1) / gdn::ssm::chunk::kTok;
+    const size_t n = (size_t)B * H * p.nc;
+    p.decs = round_up(n * dk * dv * 4, 256);
+    p.bytes = p.decs + round_up(n * 4, 256);
+    return p;
+}
+
+template <int DK, int DV>
+gdn_status launch_chunks(const Scan &c, const ChunkPlan &pl, void *ws) {
+    using namespace gdn::ssm::chunk;
+    float *ds = static_cast<float *>(ws);
+    float *decs = reinterpret_cast<float *>(static_cast<char *>(ws) + pl.decs);
+    const dim3 grid(pl.nc, c.a.B * c.a.H);
+    constexpr int s1 = StateSmem<DK, DV>::kFloats * 4, s3 = OutSmem<DK, DV>::kFloats * 4;
+    static_assert(s1 <= 232448 && s3 <= 232448, "shared memory budget");
+    if (cudaFuncSetAttribute(state_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, s1) != cudaSuccess ||
+        cudaFuncSetAttribute(out_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, s3) != cudaSuccess)
+        return GDN_ERR_CUDA;
+    {
+        gdn::LaunchScope ls("ssm_chunk_state", c.stream);
+        state_kernel<DK, DV><<<grid, kThreads, s1, c.stream>>>(c.a, ds, decs, pl.nc);
+    }
+    if (launch_status() != GDN_OK) return GDN_ERR_CUDA;
+    {
+        gdn::LaunchScope ls("ssm_chunk_carry", c.stream);
+        carry_kernel<DK, DV><<<dim3(DK * DV / 4 / kThreads, c.a.B * c.a.H), kThreads, 0, c.stream>>>(c.a, ds, decs,
+                                                                                                     pl.nc);
+    }
+    if (launch_status() != GDN_OK) return GDN_ERR_CUDA;
+    gdn::LaunchScope ls("ssm_chunk_out", c.stream);
+    out_kernel<DK, DV><<<grid, kThreads, s3, c.stream>>>(c.a, ds, pl.nc);
+    return launch_status();
+}
+
+gdn_status chunk_dims(const Scan &c, const ChunkPlan &pl, void *ws) {
+    if (c.dk == 128) return c.dv == 128 ? launch_chunks<128, 128>(c, pl, ws) : launch_chunks<128, 64>(c, pl, ws);
+    return c.dv == 128 ? launch_chunks<64, 128>(c, pl, ws) : launch_chunks<64, 64>(c, pl, ws);
+}
 
 // Head blocks (128 value columns: two heads of 64 that share a group, else one
 // head) and the segments of their walks: as many as leave one wave of CTAs.
@@ -244,7 +297,7 @@ TcPlan plan_tc(int B, int T, int H, int G, int dk, int dv) {
     p.nC = (T + gdn::ssmtc::kTok - 1) / gdn::ssmtc::kTok;
     int g = gdn::device_sm_count() / (B * p.nhb);
     if (g > p.nC / kMinSegChunks) g = p.nC / kMinSegChunks;
-    if (g < 1) g = 1;
+    if (g < 1 || p.nC < kMinSegmented) g = 1;
     const int least = (p.nC + gdn::ssmtc::kMaxSegChunks - 1) / gdn::ssmtc::kMaxSegChunks;
     if (g < least) g = least;
     p.L = (p.nC + g - 1) / g;
@@ -323,13 +376,24 @@ gdn_status tc_dims(const Scan &c, const TcPlan &pl, void *ws) {
     return pl.hb == 2 ? launch_tc<DK, 64, 2>(c, pl, ws) : launch_tc<DK, 64, 1>(c, pl, ws);
 }
 
+gdn_status check_ws(const void *ws, size_t have, size_t need) {
+    if (need == 0) return GDN_OK;
+    if (!ws) return GDN_ERR_NULL;
+    if (!aligned(ws, 256)) return GDN_ERR_ALIGN;
+    return have < need ? GDN_ERR_WORKSPACE : GDN_OK;
+}
+
 gdn_status run_scan(const Scan &c, void *ws, size_t ws_bytes) {
     if (use_tc(c.a.T, c.t)) {
         const TcPlan pl = plan_tc(c.a.B, c.a.T, c.a.H, c.a.G, c.dk, c.dv);
-        if (pl.bytes && !ws) return GDN_ERR_NULL;
-        if (pl.bytes && !aligned(ws, 256)) return GDN_ERR_ALIGN;
-        if (ws_bytes < pl.bytes) return GDN_ERR_WORKSPACE;
+        const gdn_status s = check_ws(ws, ws_bytes, pl.bytes);
+        if (s != GDN_OK) return s;
         return c.dk == 128 ? tc_dims<128>(c, pl, ws) : tc_dims<64>(c, pl, ws);
+    }
+    if (use_chunks(c.a.T, c.t)) {
+        const ChunkPlan pl = plan_chunks(c.a.B, c.a.T, c.a.H, c.dk, c.dv);
+        const gdn_status s = check_ws(ws, ws_bytes, pl.bytes);
+        return s != GDN_OK ? s : chunk_dims(c, pl, ws);
     }
     if (c.t == GDN_F32) return token_dims<float, float>(c);
     return c.dt_t == GDN_F32 ? token_dims<bf16, float>(c) : token_dims<bf16, bf16>(c);
@@ -477,7 +541,8 @@ gdn_status gdn_ssm_scan(const void *q, size_t q_batch_stride, size_t q_token_str
 
 size_t gdn_ssm_workspace_size(int B, int T, int H, int G, int dk, int dv, gdn_dtype t) {
     if (!known(t) || !scan_sizes(B, T, H, G) || !((dk == 64 || dk == 128) && (dv == 64 || dv == 128))) return 0;
-    return use_tc(T, t) ? plan_tc(B, T, H, G, dk, dv).bytes : 0;
+    if (use_tc(T, t)) return plan_tc(B, T, H, G, dk, dv).bytes;
+    return use_chunks(T, t) ? plan_chunks(B, T, H, dk, dv).bytes : 0;
 }
 
 }  // extern "C"
