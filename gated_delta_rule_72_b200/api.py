@@ -15,6 +15,7 @@ from . import _lib
 
 _TWO_PI = 2 * Fraction("3.14159265358979323846264338327950288419716939937510")
 
+_F32 = torch.float32
 _DT = {torch.float32: _lib.GDN_F32, torch.bfloat16: _lib.GDN_BF16}
 
 
@@ -244,10 +245,10 @@ def _strides(t, n):
     st, shape = t.stride(), t.shape
     if 1 not in shape[:n]:
         return st[:n]
-    w = 1
-    for d in shape[n:]:
+    w = shape[n]
+    for d in shape[n + 1:]:
         w *= d
-    return tuple([st[i] if shape[i] > 1 else w for i in range(n)])
+    return tuple([s if d > 1 else w for s, d in zip(st[:n], shape)])
 
 
 def _rows(t, name):
@@ -296,27 +297,36 @@ def short_conv(x, w, bias=None, state=None, *, silu=True, lengths=None, return_s
     each sequence of a padded batch.  Returns (y, last K-1 inputs) (the state
     None if not asked).  A new y is zero behind a sequence's end, a given
     `out` keeps what it held there."""
-    dev, code = _cuda(x, "x")
+    dev, dtype = x.device, x.dtype
+    code = _DT.get(dtype)
     if x.dim() != 3 or w.dim() != 2:
         raise ValueError("x must be [B, T, C] and w [C, K]")
     B, T, C = shape = x.shape
     K = w.shape[1]
-    _view(x, "x", x.dtype, shape, dev)
-    _dense(w, "w", torch.float32, (C, K), dev)
-    if not 2 <= K <= 4:
-        raise ValueError("w must have 2 to 4 taps, got %d" % K)
-    if bias is not None:
-        _dense(bias, "bias", torch.float32, (C,), dev)
-    if state is not None:
-        _dense(state, "state", x.dtype, (B, K - 1, C), dev)
+    sshape = (B, K - 1, C)
+    if not (code is not None and x.is_cuda and x.stride()[2] == 1 and 2 <= K <= 4 and
+            w.device == dev and w.dtype is _F32 and w.shape[0] == C and w.is_contiguous() and
+            (bias is None or bias.device == dev and bias.dtype is _F32 and bias.shape == (C,) and
+             bias.is_contiguous()) and
+            (state is None or state.device == dev and state.dtype is dtype and state.shape == sshape and
+             state.is_contiguous())):
+        _cuda(x, "x")
+        _view(x, "x", dtype, shape, dev)
+        _dense(w, "w", _F32, (C, K), dev)
+        if not 2 <= K <= 4:
+            raise ValueError("w must have 2 to 4 taps, got %d" % K)
+        if bias is not None:
+            _dense(bias, "bias", _F32, (C,), dev)
+        if state is not None:
+            _dense(state, "state", dtype, sshape, dev)
     if lengths is not None:
         _dense(lengths, "lengths", torch.int32, (B,), dev)
     y = _result(out, x, shape, lengths)
     if state_out is not None:
         if state_out is not state:
-            _dense(state_out, "state_out", x.dtype, (B, K - 1, C), dev)
+            _dense(state_out, "state_out", dtype, sshape, dev)
     elif return_state:
-        state_out = x.new_empty((B, K - 1, C))
+        state_out = x.new_empty(sshape) if state is None else torch.empty_like(state)
     bs, ts = _strides(x, 2)
     _run("gdn_short_conv", dev, _lib.load().gdn_short_conv, x.data_ptr(), bs, ts, w.data_ptr(),
          None if bias is None else bias.data_ptr(), None if state is None else state.data_ptr(),
@@ -394,39 +404,51 @@ def rotary(q, k, pos, freqs, *, interleaved=False, scale=1.0, q_out=None, k_out=
     interleaved: pairs (2j, 2j+1), else (j, j + rot/2).  q_out / k_out: where
     the results go (q / k itself: in place); new contiguous tensors by default.
     Returns (q', k')."""
-    dev, code = _cuda(q, "q")
+    dev, dtype = q.device, q.dtype
+    code = _DT.get(dtype)
     if q.dim() != 4 or (k is not None and k.dim() != 4):
         raise ValueError("q and k must be [B, T, heads, d]")
     B, T, Hq, d = shape = q.shape
-    _view(q, "q", q.dtype, shape, dev)
-    bits = 64 if pos.dtype is torch.int64 else 32 if pos.dtype is torch.int32 else 0
-    if bits == 0:
-        raise ValueError("pos must be int32 or int64")
-    axes = pos.shape[2] if pos.dim() == 3 else 1
-    _dense(pos, "pos", pos.dtype, (B, T, axes) if pos.dim() == 3 else (B, T), dev)
-    _dense(freqs, "freqs", torch.int64, (2, freqs.shape[-1]), dev)
-    rot = 2 * freqs.shape[1]
-    if rot > d:
-        raise ValueError("freqs turn %d channels, the heads have %d" % (rot, d))
+    kshape = None if k is None else (B, T, k.shape[2], d)
+    pshape = pos.shape
+    axes = pshape[2] if len(pshape) == 3 else 1
+    bits = 64 if pos.dtype is torch.int64 else 32
+    pairs = freqs.shape[-1]
+    if not (code is not None and q.is_cuda and q.stride()[3] == 1 and
+            (k is None or k.device == dev and k.dtype is dtype and k.shape == kshape and k.stride()[3] == 1) and
+            pos.device == dev and (bits == 64 or pos.dtype is torch.int32) and pshape[:2] == (B, T) and
+            len(pshape) <= 3 and pos.is_contiguous() and
+            freqs.device == dev and freqs.dtype is torch.int64 and freqs.shape == (2, pairs) and
+            freqs.is_contiguous() and 2 * pairs <= d):
+        _cuda(q, "q")
+        _view(q, "q", dtype, shape, dev)
+        if k is not None:
+            _view(k, "k", dtype, kshape, dev)
+        if pos.dtype is not torch.int64 and pos.dtype is not torch.int32:
+            raise ValueError("pos must be int32 or int64")
+        _dense(pos, "pos", pos.dtype, (B, T, axes) if len(pshape) == 3 else (B, T), dev)
+        _dense(freqs, "freqs", torch.int64, (2, pairs), dev)
+        if 2 * pairs > d:
+            raise ValueError("freqs turn %d channels, the heads have %d" % (2 * pairs, d))
     if q_out is None:
         q_out = q.new_empty(shape)
     elif q_out is not q:
-        _view(q_out, "q_out", q.dtype, shape, dev)
-    args = (q.data_ptr(), *_strides(q, 3), q_out.data_ptr(), *_strides(q_out, 3), Hq)
+        _view(q_out, "q_out", dtype, shape, dev)
+    qst = _strides(q, 3)
+    qost = qst if q_out is q else _strides(q_out, 3)
     if k is not None:
-        kshape = (B, T, k.shape[2], d)
-        _view(k, "k", q.dtype, kshape, dev)
         if k_out is None:
             k_out = k.new_empty(kshape)
         elif k_out is not k:
-            _view(k_out, "k_out", q.dtype, kshape, dev)
-        args += (k.data_ptr(), *_strides(k, 3), k_out.data_ptr(), *_strides(k_out, 3), kshape[2])
+            _view(k_out, "k_out", dtype, kshape, dev)
+        kst = _strides(k, 3)
+        kargs = (k.data_ptr(), *kst, k_out.data_ptr(), *(kst if k_out is k else _strides(k_out, 3)), kshape[2])
     elif k_out is not None:
         raise ValueError("k_out without k")
     else:
-        args += (None, 0, 0, 0, None, 0, 0, 0, 0)
-    _run("gdn_rotary", dev, _lib.load().gdn_rotary, *args, pos.data_ptr(), bits, axes, freqs.data_ptr(), scale, B, T,
-         d, rot, 1 if interleaved else 0, code)
+        kargs = (None, 0, 0, 0, None, 0, 0, 0, 0)
+    _run("gdn_rotary", dev, _lib.load().gdn_rotary, q.data_ptr(), *qst, q_out.data_ptr(), *qost, Hq, *kargs,
+         pos.data_ptr(), bits, axes, freqs.data_ptr(), scale, B, T, d, 2 * pairs, 1 if interleaved else 0, code)
     return q_out, k_out
 
 
@@ -447,37 +469,44 @@ def ssm_scan(q, k, v, dt, A, D=None, dt_bias=None, state=None, *, softplus=True,
     each sequence of a padded batch.  Returns (o, final state) (the state None
     if not asked), o in q's dtype.  A new o is zero behind a sequence's end, a
     given `out` keeps what it held there."""
-    dev, code = _cuda(q, "q")
-    dtype = q.dtype
+    dev, dtype = q.device, q.dtype
+    code = _DT.get(dtype)
     if q.dim() != 4 or v.dim() != 4 or dt.dim() != 3:
         raise ValueError("q, k must be [B, T, G, dk], v [B, T, H, dv], dt [B, T, H]")
-    B, T, G, dk = q.shape
+    B, T, G, dk = gshape = q.shape
     H, dv = v.shape[2], v.shape[3]
-    oshape, sshape = (B, T, H, dv), (B, H, dk, dv)
-    _view(q, "q", dtype, q.shape, dev)
-    _view(k, "k", dtype, q.shape, dev)
-    _view(v, "v", dtype, oshape, dev)
-    _rows(q, "q")
-    _rows(k, "k")
-    _rows(v, "v")
-    if dt.dtype is not torch.float32 and dt.dtype is not dtype:
-        raise ValueError("dt must be float32 or q's dtype")
-    _view(dt, "dt", dt.dtype, (B, T, H), dev)
-    if G < 1 or H % G:
-        raise ValueError("the %d heads of v must be a multiple of the %d groups of q and k" % (H, G))
-    _dense(A, "A", torch.float32, (H,), dev)
-    if D is not None:
-        _dense(D, "D", torch.float32, (H,), dev)
-    if dt_bias is not None:
-        _dense(dt_bias, "dt_bias", torch.float32, (H,), dev)
-    if state is not None:
-        _dense(state, "state", torch.float32, sshape, dev)
+    oshape, sshape, hshape = (B, T, H, dv), (B, H, dk, dv), (H,)
+    qst, kst, vst = q.stride(), k.stride(), v.stride()
+    if not (code is not None and q.is_cuda and k.device == dev and v.device == dev and dt.device == dev and
+            k.dtype is dtype and v.dtype is dtype and (dt.dtype is _F32 or dt.dtype is dtype) and
+            k.shape == gshape and v.shape == oshape and dt.shape == (B, T, H) and G > 0 and H % G == 0 and
+            qst[2:] == (dk, 1) and kst[2:] == (dk, 1) and vst[2:] == (dv, 1) and dt.stride()[2] == 1 and
+            A.device == dev and A.dtype is _F32 and A.shape == hshape and A.is_contiguous() and
+            (D is None or D.device == dev and D.dtype is _F32 and D.shape == hshape and D.is_contiguous()) and
+            (dt_bias is None or dt_bias.device == dev and dt_bias.dtype is _F32 and dt_bias.shape == hshape and
+             dt_bias.is_contiguous()) and
+            (state is None or state.device == dev and state.dtype is _F32 and state.shape == sshape and
+             state.is_contiguous())):
+        _cuda(q, "q")
+        for t, name, shape in ((q, "q", gshape), (k, "k", gshape), (v, "v", oshape)):
+            _view(t, name, dtype, shape, dev)
+            _rows(t, name)
+        if dt.dtype is not _F32 and dt.dtype is not dtype:
+            raise ValueError("dt must be float32 or q's dtype")
+        _view(dt, "dt", dt.dtype, (B, T, H), dev)
+        if G < 1 or H % G:
+            raise ValueError("the %d heads of v must be a multiple of the %d groups of q and k" % (H, G))
+        for t, name in ((A, "A"), (D, "D"), (dt_bias, "dt_bias")):
+            if t is not None:
+                _dense(t, name, _F32, hshape, dev)
+        if state is not None:
+            _dense(state, "state", _F32, sshape, dev)
     if lengths is not None:
         _dense(lengths, "lengths", torch.int32, (B,), dev)
     o = _result(out, q, oshape, lengths)
     if state_out is not None:
         if state_out is not state:
-            _dense(state_out, "state_out", torch.float32, sshape, dev)
+            _dense(state_out, "state_out", _F32, sshape, dev)
     elif return_state:
         state_out = A.new_empty(sshape)
     lib = _lib.load()
@@ -486,8 +515,12 @@ def ssm_scan(q, k, v, dt, A, D=None, dt_bias=None, state=None, *, softplus=True,
     if nbytes:
         ws, nbytes = _workspace(nbytes, dev, workspace)
         ws = ws.data_ptr()
-    _run("gdn_ssm_scan", dev, lib.gdn_ssm_scan, q.data_ptr(), *_strides(q, 2), k.data_ptr(), *_strides(k, 2),
-         v.data_ptr(), *_strides(v, 2), dt.data_ptr(), *_strides(dt, 2), A.data_ptr(),
+    if B == 1 or T == 1:
+        qst, kst, vst, dst = _strides(q, 2), _strides(k, 2), _strides(v, 2), _strides(dt, 2)
+    else:
+        dst = dt.stride()
+    _run("gdn_ssm_scan", dev, lib.gdn_ssm_scan, q.data_ptr(), qst[0], qst[1], k.data_ptr(), kst[0], kst[1],
+         v.data_ptr(), vst[0], vst[1], dt.data_ptr(), dst[0], dst[1], A.data_ptr(),
          None if D is None else D.data_ptr(), None if dt_bias is None else dt_bias.data_ptr(),
          None if state is None else state.data_ptr(), None if state_out is None else state_out.data_ptr(),
          o.data_ptr(), None if lengths is None else lengths.data_ptr(), B, T, H, G, dk, dv, 1 if softplus else 0, code,
