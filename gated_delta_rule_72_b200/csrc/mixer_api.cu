@@ -237,7 +237,19 @@ size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // ---------------------------------------------------------------------------
 // Chunked path of the scan on the CUDA cores (fp32)
 // ---------------------------------------------------------------------------
-bool use_chunks(int T, gdn_dtype t) { return t == GDN_F32 && T > kTokenCall; }
+// In chunks, or token by token with a warp for 8 columns?  From B200 timings:
+// the walk takes 0.21 us a token at d_k = 128 (0.18 at 64) while every warp has
+// a scheduler of its own (4 an SM), and 0.23 of that more for each further warp
+// there; the chunks take 30 us (three launches) and 0.16 us for every block of 64
+// tokens x 128 x 64, 0.19 at d_k = 64 (2,048 tokens: 24 heads of 128 x 64 125 us
+// against 436; 384 heads of 64 x 64 1,130 us against 720).
+bool use_chunks(int B, int T, int H, int dk, int dv, gdn_dtype t) {
+    if (t != GDN_F32 || T <= kTokenCall) return false;
+    const double warps = (double)B * H * dv / 8, per = warps / (4.0 * gdn::device_sm_count());
+    const double walk = T * (dk == 128 ? 0.21 : 0.18) * (per > 1 ? 0.77 + 0.23 * per : 1.0);
+    const double blocks = (double)B * H * ((T + 63) / 64) * dk * dv / (128 * 64);
+    return 30.0 + (dk == 128 ? 0.16 : 0.19) * blocks < walk;
+}
 
 struct ChunkPlan {
     int nc;
@@ -390,7 +402,7 @@ gdn_status run_scan(const Scan &c, void *ws, size_t ws_bytes) {
         if (s != GDN_OK) return s;
         return c.dk == 128 ? tc_dims<128>(c, pl, ws) : tc_dims<64>(c, pl, ws);
     }
-    if (use_chunks(c.a.T, c.t)) {
+    if (use_chunks(c.a.B, c.a.T, c.a.H, c.dk, c.dv, c.t)) {
         const ChunkPlan pl = plan_chunks(c.a.B, c.a.T, c.a.H, c.dk, c.dv);
         const gdn_status s = check_ws(ws, ws_bytes, pl.bytes);
         return s != GDN_OK ? s : chunk_dims(c, pl, ws);
@@ -542,7 +554,7 @@ gdn_status gdn_ssm_scan(const void *q, size_t q_batch_stride, size_t q_token_str
 size_t gdn_ssm_workspace_size(int B, int T, int H, int G, int dk, int dv, gdn_dtype t) {
     if (!known(t) || !scan_sizes(B, T, H, G) || !((dk == 64 || dk == 128) && (dv == 64 || dv == 128))) return 0;
     if (use_tc(T, t)) return plan_tc(B, T, H, G, dk, dv).bytes;
-    return use_chunks(T, t) ? plan_chunks(B, T, H, dk, dv).bytes : 0;
+    return use_chunks(B, T, H, dk, dv, t) ? plan_chunks(B, T, H, dk, dv).bytes : 0;
 }
 
 }  // extern "C"
