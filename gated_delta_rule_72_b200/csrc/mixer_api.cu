@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/gdn.h"
 #include "common.cuh"
 #include "host.cuh"
@@ -89,6 +91,18 @@ bool clash(const View &x, const View &y, size_t es) {
 gdn_status launch_status() { return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }
 
 constexpr int kMaxTokens = 1 << 30;
+
+// Allow `kern` the dynamic shared memory it needs, once per device.
+template <typename K>
+bool allow_smem(K *kern, int bytes, std::atomic<unsigned long long> &done) {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
 
 // ---------------------------------------------------------------------------
 // Short convolution
@@ -201,9 +215,8 @@ gdn_status launch_cols(const Scan &c) {
     unsigned int *err = gdn::wait_timeout_counter();
     if (!err) return GDN_ERR_CUDA;
     auto kern = cols_kernel<DK, DV, T, Td>;
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return GDN_ERR_CUDA;
+    static std::atomic<unsigned long long> done;
+    if (!allow_smem(kern, smem_bytes<DK, T>(kMaxWarps), done)) return GDN_ERR_CUDA;
     gdn::LaunchScope ls("ssm_cols", c.stream);
     kern<<<dim3(DV / (8 * warps), c.a.B * c.a.H), 32 * warps, smem, c.stream>>>(c.a, err);
     return launch_status();
@@ -272,9 +285,8 @@ gdn_status launch_chunks(const Scan &c, const ChunkPlan &pl, void *ws) {
     const dim3 grid(pl.nc, c.a.B * c.a.H);
     constexpr int s1 = StateSmem<DK, DV>::kFloats * 4, s3 = OutSmem<DK, DV>::kFloats * 4;
     static_assert(s1 <= 232448 && s3 <= 232448, "shared memory budget");
-    if (cudaFuncSetAttribute(state_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, s1) != cudaSuccess ||
-        cudaFuncSetAttribute(out_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, s3) != cudaSuccess)
-        return GDN_ERR_CUDA;
+    static std::atomic<unsigned long long> done1, done3;
+    if (!allow_smem(state_kernel<DK, DV>, s1, done1) || !allow_smem(out_kernel<DK, DV>, s3, done3)) return GDN_ERR_CUDA;
     {
         gdn::LaunchScope ls("ssm_chunk_state", c.stream);
         state_kernel<DK, DV><<<grid, kThreads, s1, c.stream>>>(c.a, ds, decs, pl.nc);
@@ -364,8 +376,8 @@ gdn_status launch_tc(const Scan &c, const TcPlan &pl, void *ws) {
         float *copy = a.state_in && a.state_in == a.state_out ? reinterpret_cast<float *>(base + pl.init) : nullptr;
         auto kern = tail_kernel<DK, DV, HB>;
         constexpr int smem = TailSmem<DK, DV * HB>::kBytes;
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-            return GDN_ERR_CUDA;
+        static std::atomic<unsigned long long> done;
+        if (!allow_smem(kern, smem, done)) return GDN_ERR_CUDA;
         gdn::LaunchScope ls("ssm_tail", c.stream);
         kern<<<dim3(pl.nseg - 1, a.B * pl.nhb), kTailThreads, smem, c.stream>>>(mk, mv, p, tails, decs, copy);
         if (launch_status() != GDN_OK) return GDN_ERR_CUDA;
@@ -375,8 +387,8 @@ gdn_status launch_tc(const Scan &c, const TcPlan &pl, void *ws) {
     }
     auto kern = walk_kernel<DK, DV, HB>;
     constexpr int smem = Smem<DK, DV * HB>::kBytes;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return GDN_ERR_CUDA;
+    static std::atomic<unsigned long long> done;
+    if (!allow_smem(kern, smem, done)) return GDN_ERR_CUDA;
     gdn::LaunchScope ls("ssm_walk", c.stream);
     kern<<<dim3(pl.nseg, a.B * pl.nhb), kThreads, smem, c.stream>>>(mq, mk, mv, mo, p);
     return launch_status();

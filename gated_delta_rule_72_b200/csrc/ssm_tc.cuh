@@ -280,6 +280,28 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     const bool last = nC == 0 ? seg == 0 : (c0 < nC && c1 == nC);
     if (nch <= 0 && !last) return;
 
+    auto load_x = [&](int c) {
+        uint64_t *bar = &x_full[c & 1];
+        mbar_arrive_expect_tx(bar, SM::kXSlot);
+#pragma unroll
+        for (int x = 0; x < W / 64; ++x)
+            tma_load_4d(smem + SM::kX + (c & 1) * SM::kXSlot + x * 16384, &tm_v, bar, h0 * DV + 64 * x,
+                        (c0 + c) * kTok, b, 0);
+    };
+    auto load_k = [&](int c) {
+        uint64_t *bar = &k_full[c & 1];
+        mbar_arrive_expect_tx(bar, SM::kKSlot);
+#pragma unroll
+        for (int x = 0; x < DK / 64; ++x)
+            tma_load_4d(smem + SM::kK + (c & 1) * SM::kKSlot + x * 16384, &tm_k, bar, grp * DK + 64 * x,
+                        (c0 + c) * kTok, b, 0);
+    };
+    auto load_q = [&](int c) {
+        mbar_arrive_expect_tx(q_full, SM::kKSlot);
+#pragma unroll
+        for (int x = 0; x < DK / 64; ++x)
+            tma_load_4d(smem + SM::kQ + x * 16384, &tm_q, q_full, grp * DK + 64 * x, (c0 + c) * kTok, b, 0);
+    };
     if (tid == 0) {
         const uint8_t counts[24] = {1, 1, 1, 1, 1, 1, 1, 1, kCW, 1, kMW, 1, kMW, kMW, 4, 4, 4, 1, 1, 1, 1, 1,
                                     4 + kCW + kMW, 4 + kCW + kMW};
@@ -287,9 +309,9 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         for (int i = 0; i < 24; ++i) mbar_init(bars + i, counts[i]);
         fence_mbar_init();
         *abort_s = 0;
-        prefetch_tensormap(&tm_q);
-        prefetch_tensormap(&tm_k);
-        prefetch_tensormap(&tm_v);
+        // the first chunks' tiles, while the start state is gathered
+        if (nch > 0) { load_k(0); load_q(0); load_x(0); }
+        if (nch > 1) { load_k(1); load_x(1); }
         prefetch_tensormap(&tm_o);
     }
     if (warp == 0) {
@@ -360,30 +382,6 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     if (warp == 4) {
         // ============================ loads and stores ==============================
         if (lane == 0) {
-            auto load_x = [&](int c) {
-                uint64_t *bar = &x_full[c & 1];
-                mbar_arrive_expect_tx(bar, SM::kXSlot);
-#pragma unroll
-                for (int x = 0; x < W / 64; ++x)
-                    tma_load_4d(smem + SM::kX + (c & 1) * SM::kXSlot + x * 16384, &tm_v, bar, h0 * DV + 64 * x,
-                                (c0 + c) * kTok, b, 0);
-            };
-            auto load_k = [&](int c) {
-                uint64_t *bar = &k_full[c & 1];
-                mbar_arrive_expect_tx(bar, SM::kKSlot);
-#pragma unroll
-                for (int x = 0; x < DK / 64; ++x)
-                    tma_load_4d(smem + SM::kK + (c & 1) * SM::kKSlot + x * 16384, &tm_k, bar, grp * DK + 64 * x,
-                                (c0 + c) * kTok, b, 0);
-            };
-            auto load_q = [&](int c) {
-                mbar_arrive_expect_tx(q_full, SM::kKSlot);
-#pragma unroll
-                for (int x = 0; x < DK / 64; ++x)
-                    tma_load_4d(smem + SM::kQ + x * 16384, &tm_q, q_full, grp * DK + 64 * x, (c0 + c) * kTok, b, 0);
-            };
-            if (nch > 0) { load_k(0); load_q(0); load_x(0); }
-            if (nch > 1) { load_k(1); load_x(1); }
             for (int c = 0; c < nch; ++c) {
                 if (c + 1 < nch) {
                     if (!wait(r_done, c)) break;
@@ -433,19 +431,22 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     mma_bf16(tmem + cG, adv(dQ, o), adv(dK, ks + o), idG, k > 0);
                 }
                 mma_commit(g_full);
-                // R = Q S, over the output before
                 if (!wait(s_ready, c)) break;
-                if (c > 0 && !wait(y_free, c - 1)) break;
-                tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < DK / 16; ++k)
-                    mma_bf16(tmem + cY, adv(dQ, (k >> 2) * 16384 + (k & 3) * 32),
-                             adv(dS, (k >> 2) * (W * 128) + (k & 3) * 32), idR, k > 0);
-                mma_commit(r_done);
                 // S += dS, 32 tokens at a time
                 bool ok = true;
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q, ++wph) {
+                    // R = Q S, over the output before, once the first product of dS keeps
+                    // the tensor cores busy (before it: 453 us on 4 x 16,384 x 32 x 128, so 440)
+                    if (q == 1) {
+                        if (c > 0 && !(ok = wait(y_free, c - 1))) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int k = 0; k < DK / 16; ++k)
+                            mma_bf16(tmem + cY, adv(dQ, (k >> 2) * 16384 + (k & 3) * 32),
+                                     adv(dS, (k >> 2) * (W * 128) + (k & 3) * 32), idR, k > 0);
+                        mma_commit(r_done);
+                    }
                     if (!(ok = wait(&wx_ready[q & 1], wph >> 1))) break;
                     tc_fence_after();
                     const uint32_t wx = tmem + cW + (q & 1) * 48;
@@ -863,13 +864,22 @@ tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     }
     if (c1 >= nC) return;      // the last segment of its sequence, or behind it: whole chunks only from here
 
+    auto load = [&](int i) {   // chunk i from the end
+        const int st = i % kTailStages, t0 = (c1 - 1 - i) * kTok;
+        unsigned char *dst = smem + st * SM::kStage;
+        mbar_arrive_expect_tx(&full[st], SM::kStage);
+#pragma unroll
+        for (int x = 0; x < W / 64; ++x) tma_load_4d(dst + x * 16384, &tm_v, &full[st], h0 * DV + 64 * x, t0, b, 0);
+#pragma unroll
+        for (int x = 0; x < DK / 64; ++x)
+            tma_load_4d(dst + (W / 64 + x) * 16384, &tm_k, &full[st], grp * DK + 64 * x, t0, b, 0);
+    };
     if (tid == 0) {
 #pragma unroll
         for (int i = 0; i < 15; ++i) mbar_init(bars + i, i >= 8 && i < 12 ? 16 : (i == 6 || i == 7 ? 4 : 1));
         fence_mbar_init();
         *abort_s = 0;
-        prefetch_tensormap(&tm_k);
-        prefetch_tensormap(&tm_v);
+        load(0);               // the last chunk counts whatever the decays are
     }
     if (warp == 0) {
         tmem_alloc(tmem_s, 512);
@@ -883,15 +893,24 @@ tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         bias[h] = p.a.dt_bias ? p.a.dt_bias[h0 + h] : 0.f;
     }
     const int nb = 4 * p.L;
-    for (int i = warp; i < nb; i += kTailThreads / 32) {
+    constexpr int kNW = kTailThreads / 32, kAhead = 4;        // blocks a warp loads at once
+    for (int i0 = warp; i0 < nb; i0 += kNW * kAhead) {
+        float x[kAhead][HB];
 #pragma unroll
-        for (int h = 0; h < HB; ++h) {
-            float d, s;
-            gate(p, load_dt(p, b, c0 * kTok + i * 32 + lane, h0 + h) + bias[h], true, A2[h], d, s);
+        for (int k = 0; k < kAhead; ++k)
 #pragma unroll
-            for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-            if (lane == 0) sums[h * 4 * kMaxSegChunks + i] = s;
-        }
+            for (int h = 0; h < HB; ++h)
+                x[k][h] = i0 + k * kNW < nb ? load_dt(p, b, c0 * kTok + (i0 + k * kNW) * 32 + lane, h0 + h) : 0.f;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+            for (int h = 0; h < HB; ++h) {
+                float d, s;
+                gate(p, x[k][h] + bias[h], true, A2[h], d, s);
+#pragma unroll
+                for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+                if (lane == 0 && i0 + k * kNW < nb) sums[h * 4 * kMaxSegChunks + i0 + k * kNW] = s;
+            }
     }
     tc_fence_before();
     __syncthreads();
@@ -924,22 +943,14 @@ tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         }
     }
     __syncthreads();
-    const int steps = max(steps_s[0], steps_s[HB - 1]);
+    const int steps = max(1, max(steps_s[0], steps_s[HB - 1]));   // (the first tile is on its way)
     auto wait = [&](uint64_t *bar, uint32_t ph) { return wait_phase(bar, ph, abort_s, p.err); };
 
     if (warp == 16) {
         if (lane == 0) {
-            for (int i = 0; i < steps; ++i) {
-                const int st = i % kTailStages, t0 = (c1 - 1 - i) * kTok;
-                if (i >= kTailStages && !wait(&freed[st], i / kTailStages - 1)) break;
-                unsigned char *dst = smem + st * SM::kStage;
-                mbar_arrive_expect_tx(&full[st], SM::kStage);
-#pragma unroll
-                for (int x = 0; x < W / 64; ++x)
-                    tma_load_4d(dst + x * 16384, &tm_v, &full[st], h0 * DV + 64 * x, t0, b, 0);
-#pragma unroll
-                for (int x = 0; x < DK / 64; ++x)
-                    tma_load_4d(dst + (W / 64 + x) * 16384, &tm_k, &full[st], grp * DK + 64 * x, t0, b, 0);
+            for (int i = 1; i < steps; ++i) {
+                if (i >= kTailStages && !wait(&freed[i % kTailStages], i / kTailStages - 1)) break;
+                load(i);
             }
         }
         __syncwarp();
