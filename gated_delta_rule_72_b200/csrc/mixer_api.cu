@@ -390,8 +390,19 @@ gdn_status launch_tc(const Scan &c, const TcPlan &pl, void *ws) {
     static std::atomic<unsigned long long> done;
     if (!allow_smem(kern, smem, done)) return GDN_ERR_CUDA;
     gdn::LaunchScope ls("ssm_walk", c.stream);
-    kern<<<dim3(pl.nseg, a.B * pl.nhb), kThreads, smem, c.stream>>>(mq, mk, mv, mo, p);
-    return launch_status();
+    // behind the contributions' launch the walk may start before they have all
+    // finished (it waits for them before it reads anything of theirs)
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(pl.nseg, a.B * pl.nhb);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = c.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pl.nseg > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, mo, p) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 template <int DK>

@@ -324,6 +324,8 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     const uint32_t tmem = *tmem_s;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
 
+    // with segments this grid starts beside the contributions' last blocks: what they wrote is read from here on
+    if (p.nseg > 1) asm volatile("griddepcontrol.wait;" ::: "memory");
     // The walk's start state, warps 0-15: 32 TMEM lanes (value columns) x DK/4
     // rows each, every load of a segment's contribution in flight at once.
     if (warp < 16) {
@@ -856,6 +858,7 @@ tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     const int n = gdn::ssm::live_tokens(p.a, b);
     const int nC = (n + kTok - 1) / kTok;
     const int c0 = seg * p.L, c1 = c0 + p.L;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the walk's blocks may start on free SMs
     if (seg == 0 && init_copy) {
         // the walk's start state, kept from its in-place update
         const size_t base = (size_t)(b * p.a.H + h0) * DK * DV;
