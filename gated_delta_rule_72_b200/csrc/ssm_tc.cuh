@@ -336,12 +336,8 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         float x[NR];
 #pragma unroll
         for (int i = 0; i < NR; ++i) x[i] = 0.f;
-        if (seg == 0 && p.init && v < W) {
-#pragma unroll
-            for (int i = 0; i < NR; ++i) x[i] = p.init[(bh * DK + r0 + i) * DV + vcol];
-        }
         // contributions of the segments before, latest first, down to the one
-        // behind which all has decayed (segment 0's holds the initial state)
+        // behind which all has decayed; behind the first, the initial state
         float carry = 0.f;
         for (int g1 = seg; g1 > 0 && carry >= kForgetLog; g1 -= 32) {
             const int g = g1 - 1 - lane;
@@ -362,6 +358,11 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     for (int i = 0; i < NR; ++i) x[i] = fmaf(f, src[(size_t)i * DV], x[i]);
             }
             carry += __shfl_sync(0xffffffffu, lg, 31);
+        }
+        if (p.init && carry >= kForgetLog && v < W) {
+            const float f = ex2(carry), *src = p.init + (bh * DK + r0) * DV + vcol;
+#pragma unroll
+            for (int i = 0; i < NR; ++i) x[i] = fmaf(f, src[(size_t)i * DV], x[i]);
         }
         if (nch > 0) {
 #pragma unroll
@@ -818,8 +819,7 @@ struct TailSmem {
 };
 
 // grid (nseg - 1, B * nhb): segment g of a head block: tails[g] = the state
-// after it when it starts from zero (segment 0: from the initial state),
-// decs[g] = its log2 decay.  Segments without a successor do nothing.  The
+// after it when it starts from zero, decs[g] = its log2 decay.  Segments without a successor do nothing.  The
 // chunks are taken from the last one back, until what is before has decayed
 // below kForgetLog; every product accumulates onto the state in TMEM, so that
 // the weighted values of one chunk are made while the chunk before is
@@ -1037,27 +1037,22 @@ tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             __syncwarp();
             if (lane == 0) mbar_arrive(&wx_ready[i & 1]);
         }
-        // ---- out: warps 0-7, half of d_k each
-        if (warp < 8 && wait(done, 0)) {
+        // ---- out: a quarter of d_k each
+        if (wait(done, 0)) {
             tc_fence_after();
-            constexpr int NK = DK / 2;
+            constexpr int NK = DK / 4;
             const int u = warp >> 2, v = quarter * 32 + lane;
             const int hv = v / DV < HB ? v / DV : 0, vcol = v % DV;
             const size_t bh = (size_t)(b * p.a.H + h0 + hv);
-            const float f = ex2(after_s[hv]);
-            const bool add = seg == 0 && p.a.state_in;
             float *dst = tails + ((bh * (p.nseg - 1) + seg) * DK + u * NK) * DV + vcol;
-            const float *src = p.a.state_in ? p.a.state_in + (bh * DK + u * NK) * DV + vcol : nullptr;
-#pragma unroll 1
-            for (int k = 0; k < NK; k += 16) {
-                float x[16];
-                tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + cS + u * NK + k, x);
-                tmem_wait_ld();
-                if (v < W)
+            float x[NK];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        dst[(size_t)(k + i) * DV] = add ? fmaf(f, src[(size_t)(k + i) * DV], x[i]) : x[i];
-            }
+            for (int k = 0; k < NK; k += 16)
+                tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + cS + u * NK + k, x + k);
+            tmem_wait_ld();
+            if (v < W)
+#pragma unroll
+                for (int i = 0; i < NK; ++i) dst[(size_t)i * DV] = x[i];
         }
         if (tid < HB) decs[(size_t)(b * p.a.H + h0 + tid) * (p.nseg - 1) + seg] = after_s[tid];
     }
