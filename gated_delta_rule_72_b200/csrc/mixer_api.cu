@@ -198,8 +198,8 @@ gdn_status launch_token(const Scan &c) {
 
 template <int DK, int DV, typename T, typename Td>
 gdn_status token_cols(const Scan &c) {
-    // whole heads when they fill the GPU twice, else slices of 32 columns
-    if ((long long)c.a.B * c.a.H >= 2ll * gdn::device_sm_count()) return launch_token<DK, DV, DV, T, Td>(c);
+    // slices of 64 columns when they fill the GPU twice, else of 32
+    if ((long long)c.a.B * c.a.H * (DV / 64) >= 2ll * gdn::device_sm_count()) return launch_token<DK, DV, 64, T, Td>(c);
     return launch_token<DK, DV, 32, T, Td>(c);
 }
 
