@@ -513,6 +513,8 @@ def ssm_scan(q, k, v, dt, A, D=None, dt_bias=None, state=None, *, softplus=True,
     nbytes = lib.gdn_ssm_workspace_size(B, T, H, G, dk, dv, code)
     ws = None
     if nbytes:
+        if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+            raise ValueError("workspace must be contiguous and on %s" % dev)
         ws, nbytes = _workspace(nbytes, dev, workspace)
         ws = ws.data_ptr()
     if B == 1 or T == 1:
