@@ -178,8 +178,8 @@ template <int DK, int DV>
 struct OutSmem {
     static constexpr int LQ = DK + 4, LM = kTok + 4;      // padded rows: 16-byte reads of 8 rows spread over the banks
     static constexpr int kQ = 0, kK = kQ + kTok * LQ;
-    static constexpr int kKS = kTok * (LQ > DV ? LQ : DV);                    // k, then 64 rows of the state at a time
-    static constexpr int kV = kK + kKS, kM = kV + kTok * DV, kC = kM + kTok * LM;
+    static constexpr int kKS = kTok * (LQ > DV ? LQ : DV);     // k, then the state 64 rows at a time, then v:
+    static constexpr int kM = kK + kKS, kC = kM + kTok * LM;   // one buffer, so that two blocks fit an SM
     static constexpr int kFloats = kC + 2 * kTok + 2 * kTok + 4;              // c (64 bits), d, P(i, start)
 };
 
@@ -195,7 +195,7 @@ out_kernel(const Args a, const float *__restrict__ starts, int nc)
     const int c = blockIdx.x, b = blockIdx.y / a.H, h = blockIdx.y % a.H, g = h / (a.H / a.G);
     const int n = live_tokens(a, b), t0 = c * kTok, tid = threadIdx.x, lane = tid & 31;
     if (t0 >= n) return;
-    float *qs = sm + SM::kQ, *ks = sm + SM::kK, *vs = sm + SM::kV, *ms = sm + SM::kM;
+    float *qs = sm + SM::kQ, *ks = sm + SM::kK, *vs = ks, *ms = sm + SM::kM;
     double *cs = reinterpret_cast<double *>(sm + SM::kC);
     float *dsz = sm + SM::kC + 2 * kTok, *es = dsz + kTok, *half = es + kTok;
     if (tid < 64) {
@@ -216,7 +216,6 @@ out_kernel(const Args a, const float *__restrict__ starts, int nc)
     }
     load_rows<DK, SM::LQ>(qs, static_cast<const float *>(a.q) + b * a.q_bs + (size_t)g * DK, a.q_ts, t0, n);
     load_rows<DK, SM::LQ>(ks, static_cast<const float *>(a.k) + b * a.k_bs + (size_t)g * DK, a.k_ts, t0, n);
-    load_rows<DV, DV>(vs, static_cast<const float *>(a.v) + b * a.v_bs + (size_t)h * DV, a.v_ts, t0, n);
     __syncthreads();
     // ---- M = (Q K^T) * decay * d, rows gy + 16 i, columns gx + 16 j
     {
@@ -299,6 +298,9 @@ out_kernel(const Args a, const float *__restrict__ starts, int nc)
 #pragma unroll
         for (int j = 0; j < TN / 2; ++j) acc[i][j] = make_float2(e * acc[i][j].x, e * acc[i][j].y);
     }
+    __syncthreads();
+    load_rows<DV, DV>(vs, static_cast<const float *>(a.v) + b * a.v_bs + (size_t)h * DV, a.v_ts, t0, n);
+    __syncthreads();
     add(ms, SM::LM, vs, r0 + TM);                  // (rows up to the tile's last: the rest of M is zero)
     const float D = a.D ? a.D[h] : 0.f;
     float *o = static_cast<float *>(a.o) + (((size_t)b * a.T + t0) * a.H + h) * DV + tx * 4;
