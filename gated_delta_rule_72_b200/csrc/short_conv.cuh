@@ -8,11 +8,14 @@
 // and one silu per element stay below that (two special-function operations
 // an element, 16 per SM and cycle, are 0.7 of the time of the bytes at bf16).
 // A thread owns V consecutive channels (16 bytes) for a tile of tokens: the
-// filter and the K-1 inputs before stay in registers, and a row
-// is loaded kBatch rows before it is used, so that a thread has kBatch
-// independent 16-byte loads in flight all the time.  A tile re-reads the K-1
-// rows before it.  Rows or bases that are not 16-byte aligned, and channel
-// counts that are no multiple of V, take the V = 1 form.
+// filter and the K-1 inputs before stay in registers, a row is loaded kBatch
+// rows before it is used, so that a thread has kBatch independent 16-byte loads
+// in flight all the time, and two channels share a multiply-add.  A tile
+// re-reads the K-1 rows before it.  Rows or bases that are not 16-byte aligned,
+// and channel counts that are no multiple of V, take the V = 1 form.
+// 32,760 x 4,608 bf16, K = 4 with silu: 131 us, 4.6 TB/s (without the silu 109;
+// a copy of the same bytes takes 98); three blocks an SM, with four the filter spills
+// (200 us).
 //
 // The state out is written by the threads of the first tile, which are also
 // the only readers of the state in: each thread has read its channels' state

@@ -12,9 +12,11 @@
 // prefix sums c in 64 bits: in 32 the difference of two sums near 64 would be
 // off by 4e-6.  Weights to the end and from the start are sums of their own.
 //
-// A chunk costs 64 (64 d_k + 64 d_v + 2 d_k d_v) multiply-adds, 16 of a token's
-// 2 d_k d_v spent again on the scores at d = 128; bound by the multiply-adds and
-// the shared-memory reads that feed them.
+// A chunk costs 64 (64 d_k + 64 d_v + 2 d_k d_v) multiply-adds.  Bound by the
+// shared-memory reads that feed them (a 16-byte read of a warp takes four cycles
+// even where all its lanes want the same) and, with few chunks, by the chain of
+// loads and barriers of one block: 5 sequences of up to 777 tokens, 6 heads of
+// 64 x 64, 28 us; 2,048 tokens of 24 heads of 128 x 64 123 us.
 #pragma once
 
 #include "ssm_token.cuh"

@@ -12,8 +12,10 @@
 // the inputs' own type.  The readout of four tokens and four columns is summed
 // over the row groups at once: 15 shuffles leave each lane with one sum.
 //
-// Bound by issue, about 24 + 0.4 d_k instructions a token and warp.  fp32
-// throughout, sums of d_k / 16 terms per lane.
+// Bound by the latency of a warp's own chain while each has a scheduler to itself
+// (0.21 us a token at d_k = 128: 512 tokens of 16 heads of 128 x 128 114 us), then
+// by issue, about 24 + 0.4 d_k instructions a token and warp.  fp32 throughout,
+// sums of d_k / 16 terms per lane.
 #pragma once
 
 #include "sm100.cuh"

@@ -11,34 +11,41 @@
 //   M  = G * decay * d, lower triangle, bf16, written over G in TMEM
 //   R  = Q S                              [128 x W],   S a bf16 copy of the state
 //   Y  = M V                              [128 x W],   A operand from TMEM
-//   dS = (w V)^T K                        [W x d_k],   w V as three bf16 terms
-//   o  = P(i, start) R + Y + D v ,   S <- P(end, start) S + dS  (fp32 registers)
+//   dS = (w V)^T K                        [W x d_k],   w V as three bf16 terms in TMEM
+//   o  = P(i, start) R + Y + D v ,   S <- P(end, start) S + dS
+// R is scaled where it lies and Y accumulates onto it; S stays in TMEM in fp32,
+// decayed there before dS accumulates onto it.
 //
 // Precision.  q, k, v are exact bf16 operands, so G is exact to fp32; M and the
 // operand copy of S are rounded once to bf16 (o itself is bf16: the roundings of
-// the terms stay at the size of the output's own).  The state is fp32: its
-// update takes the weighted values as three bf16 terms (24 significant bits).  Decays
-// are products of factors in (0, 1] only: a row factor (from the start of the
-// row's 32-token block) times a column factor (to that start), each a sum of
-// log-decays that is summed directly, so nothing over- or underflows that the
-// product does not; inside a 32 x 32 diagonal block 2^(c_i - c_j).
+// the terms stay at the size of the output's own; o ends 1.2 times as far from
+// its exact value as the rounding of o alone puts it).  The state is fp32: its
+// update takes the weighted values as three bf16 terms, 24 significant bits
+// (two terms left it 2.5e-6 of its norm off, three 2e-7).  Decays are products
+// of factors in (0, 1] only: a row factor (from the start of the row's 32-token
+// block) times a column factor (to that start), each a sum of log-decays that
+// is summed directly, so nothing over- or underflows that the product does
+// not; inside a 32 x 32 diagonal block 2^(c_i - c_j).
 //
-// Bound by shared-memory bandwidth (operand reads and writes), then HBM: a
-// chunk of 128 columns moves 64 KB of v and o through HBM (1,490 cycles of an
-// SM's share at 1.9 GHz) and about 580 KB through shared memory (4,500 cycles
-// at 128 B).  128-token chunks of 128 columns are the largest whose G/M, R, Y
-// and dS fit TMEM's 512 columns; sharing G between two heads of 64 halves its
-// cost and the q, k traffic.
+// What bounds it.  A chunk of 128 columns moves 64 KB of v and o through HBM
+// (1,490 cycles of an SM's share at 1.9 GHz), keeps the tensor cores busy for
+// 3,072 cycles (dS, three terms, half of it) and takes 5,600 to 6,600: the products, the
+// warps between them and the tiles' latency wait for one another in turn.
+// 4 x 16,384 tokens of 32 heads of 128 x 128 take 437 us, 3.1 TB/s (without
+// products 350, without the warps' arithmetic 336, without either 275).
+// 128-token chunks of 128 columns are the largest whose G/M, R/Y, S and
+// weighted values fit TMEM's 512 columns; sharing G between two heads of 64
+// halves its cost and the q, k traffic.
 //
 // Long walks are cut into segments that run in parallel: tail_kernel makes
 // each segment's own contribution to its final state, walking back from its
 // end until the decay has gone to zero, and the walk of segment g starts from
 // the decayed sum of the contributions before it.
 //
-// Warps: 0 loads and stores (TMA), 1 issues every MMA, 2 makes the decay
-// tables, 3-18 make M and the output, 19-26 the weighted values, 27-30 keep the
-// state.  Many warps with little code each: the roles share the instruction
-// caches, and a phase of one role is a chain of short dependent steps.
+// Warps: 0-3 keep the state, 4 loads and stores (TMA), 5 issues every MMA, 6
+// makes the decay tables, 8-11 the weighted values, 12-19 M and the output.
+// The state's warps come first because the next chunk waits for them (last,
+// with 16 warps for M: 519 us).
 #pragma once
 
 #include "sm100.cuh"
@@ -64,7 +71,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // Decays below 2^-256 are zero in fp32 many times over: per-token log-decays
 // are clamped there, which keeps the block sums exact to 2^-10.
 constexpr float kMinLog = -256.f;
-// Contributions decayed below this are dropped at a segment's start.
+// Contributions decayed below 2^-100 are dropped at a segment's start.
 constexpr float kForgetLog = -100.f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -349,7 +356,7 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 if (lane >= s) lg += y;
             }
             const float before = carry + lg - own;    // decay behind this segment
-            const int cnt = __popc(__ballot_sync(0xffffffffu, g >= 0 && (before >= kForgetLog || before == 0.f)));
+            const int cnt = __popc(__ballot_sync(0xffffffffu, g >= 0 && before >= kForgetLog));
             for (int k = 0; k < cnt; ++k) {
                 const float f = ex2(__shfl_sync(0xffffffffu, before, k));
                 const float *src = p.tails + ((bh * (p.nseg - 1) + g1 - 1 - k) * DK + r0) * DV + vcol;
@@ -823,7 +830,9 @@ struct TailSmem {
 // chunks are taken from the last one back, until what is before has decayed
 // below kForgetLog; every product accumulates onto the state in TMEM, so that
 // the weighted values of one chunk are made while the chunk before is
-// multiplied.  A chunk costs about 1,600 cycles (three products over k).
+// multiplied.  A chunk costs about 1.6 us (three products over k, 1,500 cycles
+// of them); 256 chunks of 12 head blocks in 11 segments take 40 us where some
+// heads never forget.
 template <int DK, int DV, int HB>
 __global__ void __launch_bounds__(kTailThreads, 1)
 tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Params p,

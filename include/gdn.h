@@ -358,6 +358,18 @@ GDN_API gdn_status gdn_rotary(const void *q, size_t q_batch_stride, size_t q_tok
  * through.  Values of A or d_t outside the stated ranges are not detected and
  * give unspecified results, but never out-of-bounds accesses.  Step sizes,
  * decays, sums and the state are fp32.
+ *   Paths    bf16: calls of more than 32 tokens run on the tensor cores in
+ *            chunks of 128 tokens (the masked scores and the operand copy of
+ *            the state are rounded to bf16 once: about 1.2 times the rounding
+ *            of o itself; the state keeps fp32 accuracy), long ones in
+ *            segments that run in parallel, which drops contributions that
+ *            have decayed below 2^-100.  fp32: in chunks of 64 tokens or token
+ *            by token, whichever the sizes make faster.  Within a chunk a
+ *            token whose inputs are infinite or NaN reaches the chunk's
+ *            earlier outputs too.
+ *   workspace  gdn_ssm_workspace_size(...) bytes for the same sizes on the
+ *            same device, 256-byte aligned (NULL when that is 0); calls that
+ *            may overlap in time need one each.
  */
 GDN_API gdn_status gdn_ssm_scan(const void *q, size_t q_batch_stride, size_t q_token_stride, const void *k,
                                 size_t k_batch_stride, size_t k_token_stride, const void *v, size_t v_batch_stride,

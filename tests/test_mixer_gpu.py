@@ -89,6 +89,16 @@ def test_short_conv_pieces_equal_one_call(dtype):
     assert torch.equal(torch.cat(outs, 1), want) and torch.equal(state, last)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_short_conv_far_values(dtype):
+    """Sums far out on both sides of the silu, where its exponential over- and
+    underflows."""
+    x, w, bias, state = _conv_case(1, 64, 64, 4, dtype, 8)
+    x = (x * 60).to(dtype)
+    y, last = gdn.short_conv(x, w, bias, state)
+    _check_conv(x, w, bias, state, True, None, y, last)
+
+
 # ------------------------------------------------------------------- the scan
 def _ssm_case(B, T, H, G, dk, dv, dtype, seed, dt_type=None, fast=False):
     g = _gen(seed)
