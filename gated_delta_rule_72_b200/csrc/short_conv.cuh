@@ -52,7 +52,15 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
     return r;
 }
-__device__ __forceinline__ float silu(float y) { return __fdividef(y, 1.f + __expf(-y)); }
+// y / (1 + e^-y), the exponential and the reciprocal in their forms without
+// denormals (those with them are several instructions each; below y = -87 the
+// result is -0 instead of -1e-36 and less).
+__device__ __forceinline__ float silu(float y) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return y * r;
+}
 
 template <typename T, int K, int V, bool kSilu>
 __global__ void __launch_bounds__(kThreads, kBlocks<V>)
