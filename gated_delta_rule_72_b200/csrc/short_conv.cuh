@@ -143,39 +143,60 @@ conv_kernel(const Args a)
         }
     }
 
-    for (int t = t0; t < t1; t += kBatch) {
+    // one row: the sums of the row's inputs and the K-1 before, the activation
+    auto row = [&](const Row &in, T *dst) {
+        float xi[V], out[V];
+        P::unpack(in, xi);
+        // two channels an instruction
+        if (V % 2 == 0) {
+#pragma unroll
+            for (int i = 0; i + 1 < V; i += 2) {
+                float2 acc = make_float2(bias[i], bias[i + 1]);
+#pragma unroll
+                for (int j = 0; j < K - 1; ++j)
+                    acc = fma2(make_float2(w[j][i], w[j][i + 1]), make_float2(h[j][i], h[j][i + 1]), acc);
+                acc = fma2(make_float2(w[K - 1][i], w[K - 1][i + 1]), make_float2(xi[i], xi[i + 1]), acc);
+                out[i] = acc.x;
+                out[i + 1] = acc.y;
+            }
+        } else {
+            float acc = bias[0];
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) acc = fmaf(w[j][0], h[j][0], acc);
+            out[0] = fmaf(w[K - 1][0], xi[0], acc);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+#pragma unroll
+            for (int j = 0; j + 1 < K - 1; ++j) h[j][i] = h[j + 1][i];
+            h[K - 2][i] = xi[i];
+            if (kSilu) out[i] = silu(out[i]);
+        }
+        *reinterpret_cast<Row *>(dst) = P::pack(out);
+    };
+    int t = t0;
+    const T *xp = x + (size_t)(t0 + kBatch) * a.x_ts;      // (only read where the row exists)
+    T *yp = y + (size_t)t0 * a.C;
+    for (; t + 2 * kBatch <= t1; t += kBatch) {            // batches with a whole batch behind them
+#pragma unroll
+        for (int m = 0; m < kBatch; ++m) {
+            const Row cur = r[m];
+            r[m] = *reinterpret_cast<const Row *>(xp);
+            xp += a.x_ts;
+            row(cur, yp);
+            yp += a.C;
+        }
+    }
+#pragma unroll 1
+    for (; t < t1; t += kBatch) {
 #pragma unroll
         for (int m = 0; m < kBatch; ++m) {
             if (t + m >= t1) break;
-            float xi[V], out[V];
-            P::unpack(r[m], xi);
-            if (t + m + kBatch < t1) r[m] = *reinterpret_cast<const Row *>(x + (size_t)(t + m + kBatch) * a.x_ts);
-            // two channels an instruction
-            if (V % 2 == 0) {
-#pragma unroll
-                for (int i = 0; i + 1 < V; i += 2) {
-                    float2 acc = make_float2(bias[i], bias[i + 1]);
-#pragma unroll
-                    for (int j = 0; j < K - 1; ++j)
-                        acc = fma2(make_float2(w[j][i], w[j][i + 1]), make_float2(h[j][i], h[j][i + 1]), acc);
-                    acc = fma2(make_float2(w[K - 1][i], w[K - 1][i + 1]), make_float2(xi[i], xi[i + 1]), acc);
-                    out[i] = acc.x;
-                    out[i + 1] = acc.y;
-                }
-            } else {
-                float acc = bias[0];
-#pragma unroll
-                for (int j = 0; j < K - 1; ++j) acc = fmaf(w[j][0], h[j][0], acc);
-                out[0] = fmaf(w[K - 1][0], xi[0], acc);
-            }
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-#pragma unroll
-                for (int j = 0; j + 1 < K - 1; ++j) h[j][i] = h[j + 1][i];
-                h[K - 2][i] = xi[i];
-                if (kSilu) out[i] = silu(out[i]);
-            }
-            *reinterpret_cast<Row *>(y + (size_t)(t + m) * a.C) = P::pack(out);
+            const Row cur = r[m];
+            if (t + m + kBatch < t1) r[m] = *reinterpret_cast<const Row *>(xp);
+            xp += a.x_ts;
+            row(cur, yp);
+            yp += a.C;
         }
     }
 }
