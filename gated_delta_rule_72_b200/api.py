@@ -239,18 +239,6 @@ def _refuse(t, name, dtype, shape, device):
         raise ValueError("%s must be contiguous in its last dimension" % name)
 
 
-def _strides(t, n):
-    """Strides of the first n dimensions in elements; a dimension of one entry
-    has no stride of its own (torch may report any): its row's width."""
-    st, shape = t.stride(), t.shape
-    if 1 not in shape[:n]:
-        return st[:n]
-    w = shape[n]
-    for d in shape[n + 1:]:
-        w *= d
-    return tuple([s if d > 1 else w for s, d in zip(st[:n], shape)])
-
-
 def _rows(t, name):
     """The heads of a token are contiguous: [B, T, H, d] with any batch and token stride."""
     if t.shape[2] > 1 and t.stride()[2] != t.shape[3]:
@@ -327,8 +315,8 @@ def short_conv(x, w, bias=None, state=None, *, silu=True, lengths=None, return_s
             _dense(state_out, "state_out", dtype, sshape, dev)
     elif return_state:
         state_out = x.new_empty(sshape) if state is None else torch.empty_like(state)
-    bs, ts = _strides(x, 2)
-    _run("gdn_short_conv", dev, _lib.load().gdn_short_conv, x.data_ptr(), bs, ts, w.data_ptr(),
+    xst = x.stride()
+    _run("gdn_short_conv", dev, _lib.load().gdn_short_conv, x.data_ptr(), xst[0], xst[1], w.data_ptr(),
          None if bias is None else bias.data_ptr(), None if state is None else state.data_ptr(),
          None if state_out is None else state_out.data_ptr(), y.data_ptr(),
          None if lengths is None else lengths.data_ptr(), B, T, C, K, 1 if silu else 0, code)
@@ -434,20 +422,20 @@ def rotary(q, k, pos, freqs, *, interleaved=False, scale=1.0, q_out=None, k_out=
         q_out = q.new_empty(shape)
     elif q_out is not q:
         _view(q_out, "q_out", dtype, shape, dev)
-    qst = _strides(q, 3)
-    qost = qst if q_out is q else _strides(q_out, 3)
+    qst, qost = q.stride(), q_out.stride()
     if k is not None:
         if k_out is None:
             k_out = k.new_empty(kshape)
         elif k_out is not k:
             _view(k_out, "k_out", dtype, kshape, dev)
-        kst = _strides(k, 3)
-        kargs = (k.data_ptr(), *kst, k_out.data_ptr(), *(kst if k_out is k else _strides(k_out, 3)), kshape[2])
+        kst, kost = k.stride(), k_out.stride()
+        kargs = (k.data_ptr(), kst[0], kst[1], kst[2], k_out.data_ptr(), kost[0], kost[1], kost[2], kshape[2])
     elif k_out is not None:
         raise ValueError("k_out without k")
     else:
         kargs = (None, 0, 0, 0, None, 0, 0, 0, 0)
-    _run("gdn_rotary", dev, _lib.load().gdn_rotary, q.data_ptr(), *qst, q_out.data_ptr(), *qost, Hq, *kargs,
+    _run("gdn_rotary", dev, _lib.load().gdn_rotary, q.data_ptr(), qst[0], qst[1], qst[2], q_out.data_ptr(),
+         qost[0], qost[1], qost[2], Hq, *kargs,
          pos.data_ptr(), bits, axes, freqs.data_ptr(), scale, B, T, d, 2 * pairs, 1 if interleaved else 0, code)
     return q_out, k_out
 
@@ -517,10 +505,7 @@ def ssm_scan(q, k, v, dt, A, D=None, dt_bias=None, state=None, *, softplus=True,
             raise ValueError("workspace must be contiguous and on %s" % dev)
         ws, nbytes = _workspace(nbytes, dev, workspace)
         ws = ws.data_ptr()
-    if B == 1 or T == 1:
-        qst, kst, vst, dst = _strides(q, 2), _strides(k, 2), _strides(v, 2), _strides(dt, 2)
-    else:
-        dst = dt.stride()
+    dst = dt.stride()
     _run("gdn_ssm_scan", dev, lib.gdn_ssm_scan, q.data_ptr(), qst[0], qst[1], k.data_ptr(), kst[0], kst[1],
          v.data_ptr(), vst[0], vst[1], dt.data_ptr(), dst[0], dst[1], A.data_ptr(),
          None if D is None else D.data_ptr(), None if dt_bias is None else dt_bias.data_ptr(),

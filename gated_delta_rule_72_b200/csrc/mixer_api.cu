@@ -35,6 +35,12 @@ size_t span(int B, size_t bs, int T, size_t ts, int H, size_t hs, size_t d, size
     return ((size_t)(B - 1) * bs + (size_t)(T - 1) * ts + (size_t)(H - 1) * hs + d) * es;
 }
 
+// A dimension of one entry has no stride of its own: whatever the caller gives
+// for it is replaced by the row's width.
+void settle(int n, size_t &stride, size_t width) {
+    if (n <= 1) stride = width;
+}
+
 // A [B, T, H, d] view, strides in elements.
 struct View {
     const void *p;
@@ -453,6 +459,8 @@ gdn_status gdn_short_conv(const void *x, size_t x_batch_stride, size_t x_token_s
     const size_t es = esize(dt);
     if (!aligned(w, 4) || !aligned(bias, 4) || !aligned(lengths, 4) || !aligned(x, es)) return GDN_ERR_ALIGN;
     if (!aligned(y, 16) || !aligned(state_in, 16) || !aligned(state_out, 16)) return GDN_ERR_ALIGN;
+    settle(T, x_token_stride, C);
+    settle(B, x_batch_stride, C);
     if (T > 0 && ((T > 1 && x_token_stride < (size_t)C) || (B > 1 && x_batch_stride < (size_t)C)))
         return GDN_ERR_SHAPE;
     const size_t nx = T > 0 ? span(B, x_batch_stride, T, x_token_stride, 1, 0, C, es) : 0;
@@ -481,6 +489,14 @@ gdn_status gdn_rotary(const void *q, size_t q_batch_stride, size_t q_token_strid
     if (T == 0) return GDN_OK;
     if (!q || !q_out || !pos || !freqs || (Hk > 0 && (!k || !k_out))) return GDN_ERR_NULL;
     const size_t es = esize(dt);
+    size_t *bst[4] = {&q_batch_stride, &q_out_batch_stride, &k_batch_stride, &k_out_batch_stride};
+    size_t *tst[4] = {&q_token_stride, &q_out_token_stride, &k_token_stride, &k_out_token_stride};
+    size_t *hst[4] = {&q_head_stride, &q_out_head_stride, &k_head_stride, &k_out_head_stride};
+    for (int i = 0; i < 4; ++i) {
+        settle(B, *bst[i], d);
+        settle(T, *tst[i], d);
+        settle(i < 2 ? Hq : Hk, *hst[i], d);
+    }
     const void *ps[4] = {q, q_out, Hk ? k : q, Hk ? k_out : q};
     for (const void *p : ps)
         if (!aligned(p, es)) return GDN_ERR_ALIGN;
@@ -546,6 +562,13 @@ gdn_status gdn_ssm_scan(const void *q, size_t q_batch_stride, size_t q_token_str
     const void *ps[4] = {q, k, v, o};
     for (const void *p : ps)
         if (!aligned(p, 16)) return GDN_ERR_ALIGN;
+    size_t *bst[4] = {&q_batch_stride, &k_batch_stride, &v_batch_stride, &dt_batch_stride};
+    size_t *tst[4] = {&q_token_stride, &k_token_stride, &v_token_stride, &dt_token_stride};
+    const size_t width[4] = {(size_t)G * dk, (size_t)G * dk, (size_t)H * dv, (size_t)H};
+    for (int i = 0; i < 4; ++i) {
+        settle(B, *bst[i], width[i]);
+        settle(T, *tst[i], width[i]);
+    }
     // whole 16-byte rows: tile copies need them
     const size_t st[6] = {q_batch_stride, q_token_stride, k_batch_stride, k_token_stride, v_batch_stride,
                           v_token_stride};

@@ -13,9 +13,10 @@
 // in flight all the time, and two channels share a multiply-add.  A tile
 // re-reads the K-1 rows before it.  Rows or bases that are not 16-byte aligned,
 // and channel counts that are no multiple of V, take the V = 1 form.
-// 32,760 x 4,608 bf16, K = 4 with silu: 131 us, 4.6 TB/s (without the silu 109;
-// a copy of the same bytes takes 98); three blocks an SM, with four the filter spills
-// (200 us).
+// 32,760 x 4,608 bf16, K = 4 with silu: 123 us, 4.9 TB/s (a copy of the same
+// bytes takes 98).  Three blocks an SM; with four the filter spills (155 us).  Batches
+// of 4 and 6 rows take 125 and 127 us.  The rows of all but the last two batches
+// of a tile go without bounds checks (127 us with them).
 //
 // The state out is written by the threads of the first tile, which are also
 // the only readers of the state in: each thread has read its channels' state

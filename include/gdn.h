@@ -290,7 +290,8 @@ GDN_API gdn_status gdn_readout_gate(const void *o, gdn_dtype o_dt, const void *z
  * convolution, rotary positions) and the scan without the erase term (a
  * selective state space scan).  Unlike the scans above their inputs may be
  * views: batch, token (and head) strides are in ELEMENTS, the last dimension
- * is contiguous.  Outputs are contiguous unless strides are given.
+ * is contiguous.  Outputs are contiguous unless strides are given.  The
+ * stride of a dimension of one entry is not read.
  * lengths (device, [B] int32, or NULL) gives the tokens of each sequence of a
  * padded batch, clamped to 0..T: inputs behind a sequence are not used (any
  * value, NaN too), outputs behind it are left as they were, and the final
