@@ -42,8 +42,8 @@
 // end until the decay has gone to zero, and the walk of segment g starts from
 // the decayed sum of the contributions before it.
 //
-// Warps: 0-3 keep the state, 4 loads and stores (TMA), 5 issues every MMA, 6
-// makes the decay tables, 8-11 the weighted values, 12-19 M and the output.
+// Warps: 0-3 keep the state, 4 loads and stores (TMA), 5 issues every MMA, 6 and 7
+// make the decay tables, 8-11 the weighted values, 12-19 M and the output.
 // The state's warps come first because the next chunk waits for them (last,
 // with 16 warps for M: 519 us).
 #pragma once
@@ -62,8 +62,8 @@ using gdn::tc2::swz128;
 using gdn::tc2::unpack_bf16;
 
 constexpr int kTok = 128;                  // tokens per chunk
-// Warps of the walk: 4 for the state, loads and stores, MMA issue, decay tables,
-// one idle, kCW for the weighted values, kMW for M and the output.
+// Warps of the walk: 4 for the state, loads and stores, MMA issue, two for decay
+// tables (a head each), kCW for the weighted values, kMW for M and the output.
 constexpr int kCW = 4, kMW = 8;
 constexpr int kThreads = 32 * (8 + kCW + kMW);
 constexpr unsigned long long kWaitNs = 1000000000ull;   // a wait gives up after 1 s
@@ -310,7 +310,7 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             tma_load_4d(smem + SM::kQ + x * 16384, &tm_q, q_full, grp * DK + 64 * x, (c0 + c) * kTok, b, 0);
     };
     if (tid == 0) {
-        const uint8_t counts[24] = {1, 1, 1, 1, 1, 1, 1, 1, kCW, 1, kMW, 1, kMW, kMW, 4, 4, 4, 1, 1, 1, 1, 1,
+        const uint8_t counts[24] = {1, 1, 1, 1, 1, 1, 1, 1, kCW, 1, kMW, 1, kMW, kMW, 4, 4, 4, 1, 1, 1, HB, HB,
                                     4 + kCW + kMW, 4 + kCW + kMW};
 #pragma unroll
         for (int i = 0; i < 24; ++i) mbar_init(bars + i, counts[i]);
@@ -485,74 +485,67 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             }
         }
         __syncwarp();
-    } else if (warp == 6) {
+    } else if (warp == 6 || (HB == 2 && warp == 7)) {
         // ============================ decay tables ==================================
-        float A2[HB], bias[HB], raw[HB][4];
-#pragma unroll
-        for (int h = 0; h < HB; ++h) {
-            A2[h] = p.a.A[h0 + h] * kLog2e;
-            bias[h] = p.a.dt_bias ? p.a.dt_bias[h0 + h] : 0.f;
-        }
+        // A warp for each head (one for both: 157 us, so 140, on 32,760 tokens of
+        // 24 heads of 128 x 64).
+        const int h = warp - 6;
+        const float A2 = p.a.A[h0 + h] * kLog2e;
+        const float bias = p.a.dt_bias ? p.a.dt_bias[h0 + h] : 0.f;
+        float raw[4];
         auto fetch = [&](int c) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int t = (c0 + c) * kTok + q * 32 + lane;
-#pragma unroll
-                for (int h = 0; h < HB; ++h) raw[h][q] = t < n ? load_dt(p, b, t, h0 + h) : 0.f;
+                raw[q] = t < n ? load_dt(p, b, t, h0 + h) : 0.f;
             }
         };
         if (nch > 0) fetch(0);
         for (int c = 0; c < nch; ++c) {
-            float d[HB][4], la[HB][4];
+            float d[4], la[4], suf[4], cc[4], sum[4];
 #pragma unroll
-            for (int h = 0; h < HB; ++h)
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    gate(p, raw[h][q] + bias[h], (c0 + c) * kTok + q * 32 + lane < n, A2[h], d[h][q], la[h][q]);
+            for (int q = 0; q < 4; ++q)
+                gate(p, raw[q] + bias, (c0 + c) * kTok + q * 32 + lane < n, A2, d[q], la[q]);
             if (c + 1 < nch) fetch(c + 1);
             if (c >= 2 && !wait(&tab_free[c & 1], (c >> 1) - 1)) break;
 #pragma unroll
-            for (int h = 0; h < HB; ++h) {
-                float suf[4], cc[4], sum[4];
+            for (int q = 0; q < 4; ++q) {
+                cc[q] = la[q];
+                suf[q] = __shfl_down_sync(0xffffffffu, la[q], 1);
+                if (lane == 31) suf[q] = 0.f;
+            }
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    cc[q] = la[h][q];
-                    suf[q] = __shfl_down_sync(0xffffffffu, la[h][q], 1);
-                    if (lane == 31) suf[q] = 0.f;
+                    const float u = __shfl_up_sync(0xffffffffu, cc[q], s);
+                    const float v = __shfl_down_sync(0xffffffffu, suf[q], s);
+                    if (lane >= s) cc[q] += u;
+                    if (lane + s < 32) suf[q] += v;
                 }
 #pragma unroll
-                for (int s = 1; s < 32; s <<= 1)
+            for (int q = 0; q < 4; ++q) sum[q] = __shfl_sync(0xffffffffu, cc[q], 31);
+            Table &tb = tabs[(c & 1) * 2 + h];
+            float post = 0.f;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float u = __shfl_up_sync(0xffffffffu, cc[q], s);
-                        const float v = __shfl_down_sync(0xffffffffu, suf[q], s);
-                        if (lane >= s) cc[q] += u;
-                        if (lane + s < 32) suf[q] += v;
-                    }
+            for (int q = 3; q >= 0; --q) {
+                tb.w[q * 32 + lane] = d[q] * ex2(suf[q] + post);
+                tb.c[q * 32 + lane] = cc[q];
+                tb.e[q * 32 + lane] = cc[q] - __log2f(d[q]);
+                float gap = 0.f;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) sum[q] = __shfl_sync(0xffffffffu, cc[q], 31);
-                Table &tb = tabs[(c & 1) * 2 + h];
-                float post = 0.f;
-#pragma unroll
-                for (int q = 3; q >= 0; --q) {
-                    tb.w[q * 32 + lane] = d[h][q] * ex2(suf[q] + post);
-                    tb.c[q * 32 + lane] = cc[q];
-                    tb.e[q * 32 + lane] = cc[q] - __log2f(d[h][q]);
-                    float gap = 0.f;
-#pragma unroll
-                    for (int r = q + 1; r < 4; ++r) {
-                        tb.cf[cf_off(r) + q * 32 + lane] = d[h][q] * ex2(suf[q] + gap);
-                        gap += sum[r];
-                    }
-                    post += sum[q];
+                for (int r = q + 1; r < 4; ++r) {
+                    tb.cf[cf_off(r) + q * 32 + lane] = d[q] * ex2(suf[q] + gap);
+                    gap += sum[r];
                 }
-                if (lane == 0) {
-                    tb.pre[0] = 0.f;
-                    tb.pre[1] = sum[0];
-                    tb.pre[2] = sum[0] + sum[1];
-                    tb.pre[3] = sum[0] + sum[1] + sum[2];
-                    tb.dec = ex2(post);
-                }
+                post += sum[q];
+            }
+            if (lane == 0) {
+                tb.pre[0] = 0.f;
+                tb.pre[1] = sum[0];
+                tb.pre[2] = sum[0] + sum[1];
+                tb.pre[3] = sum[0] + sum[1] + sum[2];
+                tb.dec = ex2(post);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&tab_full[c & 1]);
