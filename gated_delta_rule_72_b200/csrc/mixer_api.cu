@@ -244,10 +244,11 @@ gdn_status token_dims(const Scan &c) {
 // ---------------------------------------------------------------------------
 // Calls of at most this many tokens run token by token.
 constexpr int kTokenCall = 32;
-// Fewest chunks of a segment, and of a walk that is cut: the contributions'
-// launch costs as much as five chunks of a walk.
-constexpr int kMinSegChunks = 2;
-constexpr int kMinSegmented = 6;
+// Fewest chunks of a walk that is cut, down to segments of one chunk: with them
+// the contributions' launch takes about 5 us and a chunk of the walk 3.3 (16 heads of
+// 128 x 128: 3 chunks 17.1 us whole, 18.0 cut; 4 chunks 20.3 and 18.4; 13
+// chunks 27.9 in segments of 3, 25.4 of 2).
+constexpr int kMinSegmented = 4;
 
 bool use_tc(int T, gdn_dtype t) { return t == GDN_BF16 && T > kTokenCall; }
 
@@ -326,7 +327,7 @@ TcPlan plan_tc(int B, int T, int H, int G, int dk, int dv) {
     p.nhb = H / p.hb;
     p.nC = (T + gdn::ssmtc::kTok - 1) / gdn::ssmtc::kTok;
     int g = gdn::device_sm_count() / (B * p.nhb);
-    if (g > p.nC / kMinSegChunks) g = p.nC / kMinSegChunks;
+    if (g > p.nC) g = p.nC;
     if (g < 1 || p.nC < kMinSegmented) g = 1;
     const int least = (p.nC + gdn::ssmtc::kMaxSegChunks - 1) / gdn::ssmtc::kMaxSegChunks;
     if (g < least) g = least;
