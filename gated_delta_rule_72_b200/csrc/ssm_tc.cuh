@@ -29,10 +29,11 @@
 //
 // What bounds it.  A chunk of 128 columns moves 64 KB of v and o through HBM
 // (1,490 cycles of an SM's share at 1.9 GHz), keeps the tensor cores busy for
-// 3,072 cycles (dS, three terms, half of it) and takes 5,600 to 6,600: the products, the
+// about 3,100 cycles (dS, three terms, half of it) and takes 5,600 to 6,600: the products, the
 // warps between them and the tiles' latency wait for one another in turn.
-// 4 x 16,384 tokens of 32 heads of 128 x 128 take 437 us, 3.1 TB/s (without
-// products 350, without the warps' arithmetic 336, without either 275).
+// 4 x 16,384 tokens of 32 heads of 128 x 128 take 438 us, 3.1 TB/s (without
+// products 350, without the warps' arithmetic 336, without either 275; with v
+// loaded a chunk earlier, into a slot still in use, 426).
 // 128-token chunks of 128 columns are the largest whose G/M, R/Y, S and
 // weighted values fit TMEM's 512 columns; sharing G between two heads of 64
 // halves its cost and the q, k traffic.
@@ -559,7 +560,7 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         const int hcol = (u * NCOL) / DV;            // this warp group's head (of HB) in the output
         const float D = p.a.D ? p.a.D[h0 + hcol] : 0.f;
         const uint32_t ycol = tmem + lane_base + cY + u * NCOL;
-                const uint32_t o0 = ((u * NCOL) >> 6) * 16384 + swz128(row * 128 + ((u * NCOL) & 63) * 2);
+        const uint32_t o0 = ((u * NCOL) >> 6) * 16384 + swz128(row * 128 + ((u * NCOL) & 63) * 2);
         for (int c = 0; c < nch; ++c) {
             const Table *tb = tabs + (c & 1) * 2;
             if (!wait(&tab_full[c & 1], c >> 1)) break;
@@ -824,7 +825,7 @@ struct TailSmem {
 // below kForgetLog; every product accumulates onto the state in TMEM, so that
 // the weighted values of one chunk are made while the chunk before is
 // multiplied.  A chunk costs about 1.6 us (three products over k, 1,500 cycles
-// of them); 256 chunks of 12 head blocks in 11 segments take 40 us where some
+// of them); 256 chunks of 12 head blocks in 11 segments take 42 us where some
 // heads never forget.
 template <int DK, int DV, int HB>
 __global__ void __launch_bounds__(kTailThreads, 1)

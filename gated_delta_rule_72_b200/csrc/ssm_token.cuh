@@ -4,8 +4,8 @@
 //   S <- a S + d k v^T ,   o = S^T q + D_h v
 //
 // Bound by the state's traffic (read and written once in fp32: 268 MB for 128
-// sequences of 32 heads of 128 x 64 take 47 us, 5.7 TB/s; 256 threads a block
-// took 55).  A CTA holds CW of the d_v columns of one (b, h) state in registers:
+// sequences of 32 heads of 128 x 64 take 43 us, 6.2 TB/s; with an L2 full of
+// other data 47, and 55 with 256 threads a block).  A CTA holds CW of the d_v columns of one (b, h) state in registers:
 // thread (row group rg, column group cg) has rows rg, rg + RG, ... of four
 // consecutive columns, so that state loads and stores are 16 bytes a thread
 // and whole rows a warp, all of them in flight before the first is used.  The
