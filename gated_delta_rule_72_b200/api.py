@@ -326,6 +326,8 @@ def short_conv(x, w, bias=None, state=None, *, silu=True, lengths=None, return_s
 def short_conv_step(x, w, bias, state, *, silu=True, lengths=None, out=None):
     """One streaming call of short_conv (usually T = 1): `state` ([B,K-1,C],
     x's dtype) is updated in place.  Returns y."""
+    if state is None:
+        raise ValueError("a step needs the state that it updates")
     return short_conv(x, w, bias, state, silu=silu, lengths=lengths, out=out, state_out=state)[0]
 
 
@@ -519,5 +521,7 @@ def ssm_step(q, k, v, dt, A, state, D=None, dt_bias=None, *, softplus=True, leng
              workspace=None):
     """One streaming call of ssm_scan (usually T = 1): `state` ([B,H,dk,dv]
     fp32) is updated in place.  Returns o."""
+    if state is None:
+        raise ValueError("a step needs the state that it updates")
     return ssm_scan(q, k, v, dt, A, D, dt_bias, state, softplus=softplus, lengths=lengths, out=out, state_out=state,
                     workspace=workspace)[0]

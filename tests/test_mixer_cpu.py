@@ -165,3 +165,12 @@ def test_workspace_size_of_refused_sizes_is_zero():
     assert gdn.ssm_workspace_size(1, 256, 4, 3, 64, 64) == 0
     assert gdn.ssm_workspace_size(1, 256, 4, 1, 96, 64) == 0
     assert gdn.ssm_workspace_size(1, 0, 4, 1, 64, 64) == 0
+
+
+def test_steps_need_a_state():
+    x = torch.zeros(1, 1, 8)
+    with pytest.raises(ValueError, match="state"):
+        gdn.short_conv_step(x, torch.zeros(8, 4), None, None)
+    q = torch.zeros(1, 1, 1, 64)
+    with pytest.raises(ValueError, match="state"):
+        gdn.ssm_step(q, q, q, torch.zeros(1, 1, 1), torch.zeros(1), None)
