@@ -177,3 +177,14 @@ def test_heads_shared_by_a_group_match_heads_of_their_own():
     own = dict(c, q=c["q"].repeat_interleave(3, 2), k=c["k"].repeat_interleave(3, 2))
     b = gdn.ssm_scan(**own)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("B,T,H", [(1, 385, 1), (3, 512, 2), (1, 513, 4), (1, 5001, 1)])
+def test_segments_of_one_and_of_few_chunks(B, T, H):
+    """The shortest walks that are cut, and one head's long one, whose segments
+    remember every segment before them."""
+    c = _ssm_case(B, T, H, 1, 128, 128, BF16, T)
+    c["A"] = -torch.tensor([1e-4, 8.0, 0.0, 0.05][:H], device="cuda")
+    (o, s), names = _kernels(lambda: gdn.ssm_scan(**c))
+    assert names == {"ssm_tail", "ssm_walk"}, names
+    _check_ssm(c, o, s)
