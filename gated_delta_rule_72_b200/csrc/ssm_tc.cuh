@@ -266,13 +266,14 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     uint64_t *m_ready = bars + 10;     // M written, R scaled
     uint64_t *y_full = bars + 11;      // Y complete
     uint64_t *y_free = bars + 12;      // Y read out
-    uint64_t *y_staged = bars + 13;    // output tile written
-    uint64_t *s_ready = bars + 14;     // state decayed in TMEM, its copy written
-    uint64_t *wx_ready = bars + 15;    // [2] weighted values written
-    uint64_t *wx_free = bars + 17;     // [2] ... and read
-    uint64_t *s_full = bars + 19;      // state updated
-    uint64_t *tab_full = bars + 20;    // [2] decay tables written
-    uint64_t *tab_free = bars + 22;    // [2] ... and read
+    uint64_t *y_staged = bars + 13;    // [2] output tile written (a barrier a slot: chunk c + 1 may be done before
+                                       // the storing warp looks at chunk c's, chunk c + 2 not)
+    uint64_t *s_ready = bars + 15;     // state decayed in TMEM, its copy written
+    uint64_t *wx_ready = bars + 16;    // [2] weighted values written
+    uint64_t *wx_free = bars + 18;     // [2] ... and read
+    uint64_t *s_full = bars + 20;      // state updated
+    uint64_t *tab_full = bars + 21;    // [2] decay tables written
+    uint64_t *tab_free = bars + 23;    // [2] ... and read
     uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + SM::kCtl);
     volatile int *abort_s = reinterpret_cast<volatile int *>(smem + SM::kCtl + 4);
     Table *tabs = reinterpret_cast<Table *>(smem + SM::kTab);
@@ -311,10 +312,10 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             tma_load_4d(smem + SM::kQ + x * 16384, &tm_q, q_full, grp * DK + 64 * x, (c0 + c) * kTok, b, 0);
     };
     if (tid == 0) {
-        const uint8_t counts[24] = {1, 1, 1, 1, 1, 1, 1, 1, kCW, 1, kMW, 1, kMW, kMW, 4, 4, 4, 1, 1, 1, HB, HB,
+        const uint8_t counts[25] = {1, 1, 1, 1, 1, 1, 1, 1, kCW, 1, kMW, 1, kMW, kMW, kMW, 4, 4, 4, 1, 1, 1, HB, HB,
                                     4 + kCW + kMW, 4 + kCW + kMW};
 #pragma unroll
-        for (int i = 0; i < 24; ++i) mbar_init(bars + i, counts[i]);
+        for (int i = 0; i < 25; ++i) mbar_init(bars + i, counts[i]);
         fence_mbar_init();
         *abort_s = 0;
         // the first chunks' tiles, while the start state is gathered
@@ -402,7 +403,7 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     if (!wait(&k_free[c & 1], c >> 1)) break;
                     load_k(c + 2);
                 }
-                if (!wait(y_staged, c)) break;
+                if (!wait(&y_staged[c & 1], c >> 1)) break;
                 if (!own_rows(c)) {
 #pragma unroll
                     for (int x = 0; x < W / 64; ++x)
@@ -673,7 +674,7 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(y_free);
-                mbar_arrive(y_staged);
+                mbar_arrive(&y_staged[c & 1]);
             }
         }
     } else if (warp >= 8) {
