@@ -133,6 +133,12 @@ __device__ __forceinline__ bool mbar_wait_ns(uint64_t *bar, uint32_t parity, uns
         if (global_ns() - t0 > limit_ns) return false;
     return true;
 }
+// For a kernel that gives up: wait, for at most 10 ms, until the last of `uses`
+// phases begun on `bar` is complete (a copy or product still in flight would
+// write shared memory or TMEM that is no longer the kernel's).
+__device__ __forceinline__ void mbar_drain(uint64_t *bar, int uses) {
+    if (uses > 0) mbar_wait_ns(bar, (uint32_t)(uses - 1) & 1u, 10000000ull);
+}
 // Spin until *p >= v (acquire), for at most `limit_ns`; false on timeout.
 __device__ __forceinline__ bool spin_until_geq(const unsigned int *p, unsigned int v,
                                                unsigned long long limit_ns) {

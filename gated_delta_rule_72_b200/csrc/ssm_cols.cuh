@@ -96,12 +96,10 @@ cols_kernel(const Args a, unsigned int *err)
     const int sb = stage_bytes<DK, T>(warps), row = 2 * DK;
     const int v_off = kTok * row * (int)sizeof(T), g_off = v_off + kTok * cw * (int)sizeof(T);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStages * sb);
-    int *gave_up = reinterpret_cast<int *>(full + kStages);
     if (tid == 0) {
 #pragma unroll
         for (int s = 0; s < kStages; ++s) mbar_init(full + s, 1);
         fence_mbar_init();
-        *gave_up = 0;
     }
     __syncthreads();
 
@@ -162,10 +160,12 @@ cols_kernel(const Args a, unsigned int *err)
             S[m][i][3] = make_float2(x.w, y.w);
         }
 
-    for (int s = 0; s < ns; ++s) {
-        if (!mbar_wait_ns(full + s % kStages, (s / kStages) & 1, kWaitNs)) *gave_up = 1;
-        __syncthreads();                          // stage s and its gates are there, stage s - 1 is read
-        if (*gave_up) break;
+    bool gave_up = false;                         // the same in every thread
+    int s = 0;
+    for (; s < ns; ++s) {
+        const bool there = mbar_wait_ns(full + s % kStages, (s / kStages) & 1, kWaitNs);
+        gave_up = __syncthreads_or(!there);       // stage s and its gates are there, stage s - 1 is read
+        if (gave_up) break;
         if (tid < 32) fetch(s + kStages - 1);
         const unsigned char *st = smem + (s % kStages) * sb;
         const T *kq = reinterpret_cast<const T *>(st) + 4 * rg;
@@ -218,9 +218,11 @@ cols_kernel(const Args a, unsigned int *err)
                 o[(size_t)(t0 + tt) * a.H * DV] = from_f32<T>(fmaf(D, to_f32(vs[tt * cw + (rg & 3)]), y[0]));
         }
     }
-    if (*gave_up) {
+    if (gave_up) {
         if (tid == 0) atomicAdd(err, 1u);
-        for (int s = 0; s < kStages; ++s) mbar_wait(full + s, 0, 64);   // let copies in flight land
+        // the copies in flight land before shared memory goes
+        const int issued = min(ns, s + kStages - 1);
+        for (int i = 0; i < kStages; ++i) mbar_drain(full + i, (issued + kStages - 1 - i) / kStages);
         return;
     }
     if (a.state_out)

@@ -119,6 +119,11 @@ static __device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, vo
 __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t ph, volatile int *abort_s, unsigned int *err) {
     return mbar_try_wait(bar, ph & 1u) || wait_slow(bar, ph & 1u, abort_s, err);
 }
+// A wait gave up: the products issued by this thread end before shared memory and TMEM go.
+__device__ __forceinline__ void drain_products(uint64_t *bar) {
+    mma_commit(bar);
+    mbar_drain(bar, 1);
+}
 // D[tmem] (+)= A[tmem] * B[smem]: A is M x 16 bf16, two K elements a column.
 __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                             uint32_t accumulate) {
@@ -274,6 +279,7 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     uint64_t *s_full = bars + 20;      // state updated
     uint64_t *tab_full = bars + 21;    // [2] decay tables written
     uint64_t *tab_free = bars + 23;    // [2] ... and read
+    uint64_t *drained = bars + 25;     // products complete, when a wait gave up
     uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + SM::kCtl);
     volatile int *abort_s = reinterpret_cast<volatile int *>(smem + SM::kCtl + 4);
     Table *tabs = reinterpret_cast<Table *>(smem + SM::kTab);
@@ -312,10 +318,10 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             tma_load_4d(smem + SM::kQ + x * 16384, &tm_q, q_full, grp * DK + 64 * x, (c0 + c) * kTok, b, 0);
     };
     if (tid == 0) {
-        const uint8_t counts[25] = {1, 1, 1, 1, 1, 1, 1, 1, kCW, 1, kMW, 1, kMW, kMW, kMW, 4, 4, 4, 1, 1, 1, HB, HB,
-                                    4 + kCW + kMW, 4 + kCW + kMW};
+        const uint8_t counts[26] = {1, 1, 1, 1, 1, 1, 1, 1, kCW, 1, kMW, 1, kMW, kMW, kMW, 4, 4, 4, 1, 1, 1, HB, HB,
+                                    4 + kCW + kMW, 4 + kCW + kMW, 1};
 #pragma unroll
-        for (int i = 0; i < 25; ++i) mbar_init(bars + i, counts[i]);
+        for (int i = 0; i < 26; ++i) mbar_init(bars + i, counts[i]);
         fence_mbar_init();
         *abort_s = 0;
         // the first chunks' tiles, while the start state is gathered
@@ -394,14 +400,17 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     if (warp == 4) {
         // ============================ loads and stores ==============================
         if (lane == 0) {
+            int nq = min(nch, 1), nk = min(nch, 2), nx = nk;         // loads issued
             for (int c = 0; c < nch; ++c) {
                 if (c + 1 < nch) {
                     if (!wait(r_done, c)) break;
                     load_q(c + 1);
+                    ++nq;
                 }
                 if (c + 2 < nch) {
                     if (!wait(&k_free[c & 1], c >> 1)) break;
                     load_k(c + 2);
+                    ++nk;
                 }
                 if (!wait(&y_staged[c & 1], c >> 1)) break;
                 if (!own_rows(c)) {
@@ -414,9 +423,17 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 if (c + 2 < nch) {
                     bulk_wait_read_all();
                     load_x(c + 2);
+                    ++nx;
                 }
             }
             bulk_wait_all();
+            if (*abort_s) {        // a wait gave up: the loads land before shared memory goes
+                mbar_drain(q_full, nq);
+                for (int s = 0; s < 2; ++s) {
+                    mbar_drain(&k_full[s], (nk + 1 - s) >> 1);
+                    mbar_drain(&x_full[s], (nx + 1 - s) >> 1);
+                }
+            }
         }
         __syncwarp();
     } else if (warp == 5) {
@@ -485,6 +502,7 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                                     adv(dV, h * 16384 + s * 2048), idY, 1);
                 mma_commit(y_full);
             }
+            if (*abort_s) drain_products(drained);
         }
         __syncwarp();
     } else if (warp == 6 || (HB == 2 && warp == 7)) {
@@ -791,12 +809,6 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         }
     }
 
-    __syncthreads();
-    if (*abort_s && tid == 0) {
-        // a wait gave up: let copies and MMAs in flight land before shared memory and TMEM go
-        uint64_t *in_flight[] = {&x_full[0], &x_full[1], &k_full[0], &k_full[1], q_full, g_full, r_done, s_full, y_full};
-        for (uint64_t *bar : in_flight) mbar_wait(bar, 0, 64);
-    }
     tc_fence_before();
     __syncthreads();
     if (warp == 0) tmem_dealloc(tmem, 512);
@@ -952,12 +964,14 @@ tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     __syncthreads();
     const int steps = max(1, max(steps_s[0], steps_s[HB - 1]));   // (the first tile is on its way)
     auto wait = [&](uint64_t *bar, uint32_t ph) { return wait_phase(bar, ph, abort_s, p.err); };
+    int issued = 1;                                               // loads (known to lane 0 of warp 16)
 
     if (warp == 16) {
         if (lane == 0) {
             for (int i = 1; i < steps; ++i) {
                 if (i >= kTailStages && !wait(&freed[i % kTailStages], i / kTailStages - 1)) break;
                 load(i);
+                ++issued;
             }
         }
         __syncwarp();
@@ -1061,10 +1075,10 @@ tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         if (tid < HB) decs[(size_t)(b * p.a.H + h0 + tid) * (p.nseg - 1) + seg] = after_s[tid];
     }
     __syncthreads();
-    if (*abort_s && tid == 0) {
-        // a wait gave up: let copies and MMAs in flight land before shared memory and TMEM go
-        for (int i = 0; i < kTailStages; ++i) mbar_wait(&full[i], 0, 64);
-        mbar_wait(done, 0, 64);
+    if (*abort_s && warp == 16 && lane == 0) {
+        // a wait gave up: copies and products end before shared memory and TMEM go
+        for (int s = 0; s < kTailStages; ++s) mbar_drain(&full[s], (issued + kTailStages - 1 - s) / kTailStages);
+        mbar_drain(done, 1);
     }
     tc_fence_before();
     __syncthreads();

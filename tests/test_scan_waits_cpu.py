@@ -261,3 +261,48 @@ def test_one_barrier_for_both_output_tiles_would_not_do():
     started = [("k_full", 0), ("q_full", 0), ("x_full", 0), ("k_full", 1), ("x_full", 1)]
     bad = _faults(lambda: _Run(programs, counts, started))
     assert {b[2][0][0] for b in bad} == {"y_staged"} and {b[0][0] for b in bad} == {"loads"}, bad
+
+
+# ---- a kernel that gives up: what is in flight lands before it returns
+def _drains(text):
+    """(barrier, uses) of every wait of a kernel's way out."""
+    return re.findall(r"mbar_drain\(&?(\w+(?:\[s\]| \+ i)?), ((?:[^()]|\([^()]*\))*)\);", text)
+
+
+def _cols_source():
+    with open(os.path.join(os.path.dirname(SRC), "ssm_cols.cuh")) as f:
+        return f.read()
+
+
+def _uses(drains, bar, **env):
+    expr = dict(drains)[bar].replace("/", "//")
+    return eval(expr, {}, env)
+
+
+def test_no_wait_of_the_way_out_names_a_fixed_phase():
+    """The phase of a copy in flight depends on how many there were before it."""
+    for text in (_kernel("walk_kernel"), _kernel("tail_kernel"), _cols_source()):
+        assert not re.findall(r"\bmbar_wait(?:_ns)?\([^;]*?, 0, ", text)
+        assert _drains(text)
+
+
+def test_the_way_out_waits_for_the_last_load_of_every_slot():
+    walk, tail, cols = _drains(_kernel("walk_kernel")), _drains(_kernel("tail_kernel")), _drains(_cols_source())
+    assert {b for b, _ in walk} == {"q_full", "k_full[s]", "x_full[s]"}
+    assert "if (*abort_s) drain_products(drained);" in _kernel("walk_kernel")
+    assert {b for b, _ in tail} == {"full[s]", "done"} and {b for b, _ in cols} == {"full + i"}
+    for n in range(12):
+        assert _uses(walk, "q_full", nq=n) == n
+        for s in range(2):
+            want = len([c for c in range(n) if c % 2 == s])
+            assert _uses(walk, "k_full[s]", nk=n, s=s) == want and _uses(walk, "x_full[s]", nx=n, s=s) == want
+        for s in range(3):
+            assert _uses(tail, "full[s]", issued=n, kTailStages=3, s=s) == len([c for c in range(n) if c % 3 == s])
+        for s in range(4):
+            assert _uses(cols, "full + i", issued=n, kStages=4, i=s) == len([c for c in range(n) if c % 4 == s])
+
+
+def test_threads_of_a_block_agree_that_a_wait_gave_up():
+    """What each thread's wait came to is joined by the barrier itself: a flag
+    read behind it could be raised by a thread that is a step ahead."""
+    assert "__syncthreads_or" in _cols_source()
