@@ -357,13 +357,16 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         for (int g1 = seg; g1 > 0 && carry >= kForgetLog; g1 -= 32) {
             const int g = g1 - 1 - lane;
             const float own = g >= 0 ? p.decs[bh * (p.nseg - 1) + g] : 0.f;
-            float lg = own;                           // decay of this segment and those behind it
+            // decay behind this segment, summed without its own: taking that off again would
+            // leave nothing of small decays behind one that forgets all
+            float lg = __shfl_up_sync(0xffffffffu, own, 1);
+            if (lane == 0) lg = 0.f;
 #pragma unroll
             for (int s = 1; s < 32; s <<= 1) {
                 const float y = __shfl_up_sync(0xffffffffu, lg, s);
                 if (lane >= s) lg += y;
             }
-            const float before = carry + lg - own;    // decay behind this segment
+            const float before = carry + lg;
             const int cnt = __popc(__ballot_sync(0xffffffffu, g >= 0 && before >= kForgetLog));
             for (int k = 0; k < cnt; ++k) {
                 const float f = ex2(__shfl_sync(0xffffffffu, before, k));
@@ -372,7 +375,7 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 #pragma unroll
                     for (int i = 0; i < NR; ++i) x[i] = fmaf(f, src[(size_t)i * DV], x[i]);
             }
-            carry += __shfl_sync(0xffffffffu, lg, 31);
+            carry = __shfl_sync(0xffffffffu, before + own, 31);
         }
         if (p.init && carry >= kForgetLog && v < W) {
             const float f = ex2(carry), *src = p.init + (bh * DK + r0) * DV + vcol;
