@@ -60,7 +60,7 @@ __device__ __forceinline__ void gate(const Args &a, int b, int h, int t, int n, 
     if (t < n) {
         const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
         d = step_size(static_cast<const float *>(a.dt)[b * a.dt_bs + (size_t)t * a.dt_ts + h] + bias, a.softplus);
-        la = fmaxf(d * a.A[h] * kLog2e, kMinLog);
+        la = fmaxf(log_decay(d, a.A[h]) * kLog2e, kMinLog);
     }
 }
 

@@ -134,7 +134,7 @@ cols_kernel(const Args a, unsigned int *err)
         }
         if (half == 0) {
             const float d = t < nt ? step_size(x, a.softplus) : 0.f;
-            reinterpret_cast<float2 *>(st + g_off)[t] = make_float2(expf(d * A), d);
+            reinterpret_cast<float2 *>(st + g_off)[t] = make_float2(expf(log_decay(d, A)), d);
         }
     };
     const int ns = (n + kTok - 1) / kTok;

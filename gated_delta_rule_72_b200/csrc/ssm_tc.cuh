@@ -223,7 +223,7 @@ __device__ __forceinline__ float load_dt(const Params &p, int b, int t, int h) {
 // Step size and log2 decay of a token (zero behind the sequence's end).
 __device__ __forceinline__ void gate(const Params &p, float x, bool live, float A2, float &d, float &la) {
     d = live ? gdn::ssm::step_size(x, p.a.softplus) : 0.f;
-    la = fmaxf(d * A2, kMinLog);
+    la = fmaxf(gdn::ssm::log_decay(d, A2), kMinLog);
 }
 
 // ---------------------------------------------------------------------------

@@ -38,6 +38,10 @@ __device__ __forceinline__ float step_size(float x, int softplus) {
     return softplus ? fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))) : x;
 }
 
+// Log decay of a token.  A token without a step (and a place behind the
+// sequence's end) forgets nothing, whatever A is: -inf times 0 would be NaN.
+__device__ __forceinline__ float log_decay(float d, float A) { return d == 0.f ? 0.f : d * A; }
+
 constexpr int kTokThreads = 128;
 
 // grid (DV / CW, B * H)
@@ -73,7 +77,7 @@ token_kernel(const Args a)
         for (int i = tid; i < CW; i += kTokThreads) vs[i] = to_f32(v[i]);
         const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
         const float d = step_size(to_f32(static_cast<const Td *>(a.dt)[b * a.dt_bs + h]) + bias, a.softplus);
-        const float al = expf(d * a.A[h]);
+        const float al = expf(log_decay(d, a.A[h]));
         __syncthreads();
         const float4 vv = *reinterpret_cast<const float4 *>(&vs[cg * 4]);
         const float4 u = make_float4(d * vv.x, d * vv.y, d * vv.z, d * vv.w);

@@ -350,7 +350,9 @@ GDN_API gdn_status gdn_rotary(const void *q, size_t q_batch_stride, size_t q_tok
  *   q, k     [B, T, G, dk] `t`: G groups, each shared by H / G heads
  *   v, o     [B, T, H, dv] `t`; o contiguous
  *   dt       [B, T, H] `dt_t`: fp32, or bf16 when t is bf16
- *   A        [H] fp32, <= 0;  D, dt_bias [H] fp32 or NULL (zero); d_t >= 0
+ *   A        [H] fp32, <= 0 (-inf too: every token with a step clears the
+ *            state);  D, dt_bias [H] fp32 or NULL (zero); d_t >= 0, a token
+ *            with d_t = 0 changes nothing whatever A is
  *   state_*  [B, H, dk, dv] fp32, as in gdn_scan_causal (state_out may be
  *            state_in)
  * Pointers and the strides of q, k and v (in bytes) are multiples of 16, dt
