@@ -23,6 +23,7 @@
 // before it writes them, so the state may be updated in place.
 #pragma once
 
+#include "packed.cuh"
 #include "vecio.cuh"
 
 namespace gdn {
@@ -43,16 +44,6 @@ struct Args {
     int B, T, C, tile, ntile;  // tile: tokens per thread, a multiple of kBatch
 };
 
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 r;
-    asm("{\n\t.reg .b64 a, b, c, r;\n\t"
-        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-        "fma.rn.f32x2 r, a, b, c;\n\t"
-        "mov.b64 {%0, %1}, r;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return r;
-}
 // y / (1 + e^-y), the exponential and the reciprocal in their forms without
 // denormals (those with them are several instructions each; below y = -87 the
 // result is -0 instead of -1e-36 and less).

@@ -19,6 +19,7 @@
 // 64 x 64, 28 us; 2,048 tokens of 24 heads of 128 x 64 123 us.
 #pragma once
 
+#include "packed.cuh"
 #include "ssm_token.cuh"
 
 namespace gdn {
@@ -29,17 +30,6 @@ constexpr int kTok = 64;
 constexpr int kThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinLog = -1024.f;      // a token's log2 decay: far below what fp32 holds
-
-__device__ __forceinline__ float2 fma2(float a, float2 b, float2 c) {
-    float2 r;
-    asm("{\n\t.reg .b64 a, b, c, r;\n\t"
-        "mov.b64 a, {%2, %2};\n\tmov.b64 b, {%3, %4};\n\tmov.b64 c, {%5, %6};\n\t"
-        "fma.rn.f32x2 r, a, b, c;\n\t"
-        "mov.b64 {%0, %1}, r;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return r;
-}
 
 // Rows t0 .. t0 + 63 of a [T, ts] matrix, D columns, into rows of LD floats;
 // rows from n on are zero.

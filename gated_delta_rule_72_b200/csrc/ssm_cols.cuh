@@ -18,6 +18,7 @@
 // sums of d_k / 16 terms per lane.
 #pragma once
 
+#include "packed.cuh"
 #include "sm100.cuh"
 #include "ssm_token.cuh"
 #include "tc_common.cuh"
@@ -42,26 +43,6 @@ __host__ __device__ constexpr int stage_bytes(int warps) {
 template <int DK, typename T>
 constexpr int smem_bytes(int warps) { return kStages * stage_bytes<DK, T>(warps) + 64; }
 
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 r;
-    asm("{\n\t.reg .b64 a, b, c, r;\n\t"
-        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-        "fma.rn.f32x2 r, a, b, c;\n\t"
-        "mov.b64 {%0, %1}, r;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return r;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 r;
-    asm("{\n\t.reg .b64 a, b, r;\n\t"
-        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-        "mul.rn.f32x2 r, a, b;\n\t"
-        "mov.b64 {%0, %1}, r;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
 // Four consecutive elements from shared memory.
 __device__ __forceinline__ void load4(const float *p, float2 &a, float2 &b) {
     const float4 v = *reinterpret_cast<const float4 *>(p);

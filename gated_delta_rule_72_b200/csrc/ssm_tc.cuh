@@ -49,6 +49,7 @@
 // with 16 warps for M: 519 us).
 #pragma once
 
+#include "packed.cuh"
 #include "sm100.cuh"
 #include "ssm_token.cuh"
 #include "tc_common.cuh"
@@ -79,16 +80,6 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 r;
-    asm("{\n\t.reg .b64 a, b, r;\n\t"
-        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-        "mul.rn.f32x2 r, a, b;\n\t"
-        "mov.b64 {%0, %1}, r;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
 }
 // One lane of a converged warp, in the form that lets the compiler keep MMA
 // operands in uniform registers: behind a plain `lane == 0` each MMA cost
@@ -135,16 +126,6 @@ __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
-__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
-    float2 r;
-    asm("{\n\t.reg .b64 a, b, r;\n\t"
-        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-        "sub.rn.f32x2 r, a, b;\n\t"
-        "mov.b64 {%0, %1}, r;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
 // x = hi + mid + lo, three bf16 terms for 24 significant bits: hi and mid are
 // cut off (their rest is exact), lo is rounded.
 __device__ __forceinline__ void split3(float2 x, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
