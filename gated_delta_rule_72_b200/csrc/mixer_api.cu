@@ -110,6 +110,19 @@ bool allow_smem(K *kern, int bytes, std::atomic<unsigned long long> &done) {
     return true;
 }
 
+// A kernel that shares its registers out anew was launched with what the shares
+// need: with fewer, the warps that ask for more would wait for good.
+template <typename K>
+bool has_registers(K *kern, int need, std::atomic<int> &known) {
+    int n = known.load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaFuncAttributes at;
+        if (cudaFuncGetAttributes(&at, kern) != cudaSuccess) return false;
+        known.store(n = at.numRegs, std::memory_order_relaxed);
+    }
+    return n >= need;
+}
+
 // ---------------------------------------------------------------------------
 // Short convolution
 // ---------------------------------------------------------------------------
@@ -401,7 +414,8 @@ gdn_status launch_tc(const Scan &c, const TcPlan &pl, void *ws) {
     auto kern = walk_kernel<DK, DV, HB>;
     constexpr int smem = Smem<DK, DV * HB>::kBytes;
     static std::atomic<unsigned long long> done;
-    if (!allow_smem(kern, smem, done)) return GDN_ERR_CUDA;
+    static std::atomic<int> regs;
+    if (!allow_smem(kern, smem, done) || !has_registers(kern, kRegsLaunch, regs)) return GDN_ERR_CUDA;
     gdn::LaunchScope ls("ssm_walk", c.stream);
     // behind the contributions' launch the walk may start before they have all
     // finished (it waits for them before it reads anything of theirs)

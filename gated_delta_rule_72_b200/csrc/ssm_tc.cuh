@@ -13,15 +13,19 @@
 //   Y  = M V                              [128 x W],   A operand from TMEM
 //   dS = (w V)^T K                        [W x d_k],   w V as three bf16 terms in TMEM
 //   o  = P(i, start) R + Y + D v ,   S <- P(end, start) S + dS
-// R is scaled where it lies and Y accumulates onto it; S stays in TMEM in fp32,
-// decayed there before dS accumulates onto it.
+// R is scaled where it lies and Y accumulates onto it; S stays in the registers of
+// four warps in fp32, a value column a thread, and takes in each chunk's dS there.
 //
 // Precision.  q, k, v are exact bf16 operands, so G is exact to fp32; M and the
 // operand copy of S are rounded once to bf16 (o itself is bf16: the roundings of
 // the terms stay at the size of the output's own; o ends 1.2 times as far from
 // its exact value as the rounding of o alone puts it).  The state is fp32: its
-// update takes the weighted values as three bf16 terms, 24 significant bits
-// (two terms left it 2.5e-6 of its norm off, three 2e-7).  Decays are products
+// update takes the weighted values as three bf16 terms, 24 significant bits, and
+// sums 24 products from zero in TMEM, whose accumulators cut off what does not fit
+// 24 bits, small terms first, before the registers' addition rounds to nearest: 5e-7 of
+// its norm off at most, however long the walk (accumulated in TMEM from chunk to chunk
+// every product's cut was one of the whole state: 2e-5 behind 22 chunks of a head
+// that never forgets, and growing with their number).  Decays are products
 // of factors in (0, 1] only: a row factor (from the start of the row's 32-token
 // block) times a column factor (to that start), each a sum of log-decays that
 // is summed directly, so nothing over- or underflows that the product does
@@ -68,8 +72,8 @@ constexpr int kTok = 128;                  // tokens per chunk
 // tables (a head each), kCW for the weighted values, kMW for M and the output.
 constexpr int kCW = 4, kMW = 8;
 constexpr int kThreads = 32 * (8 + kCW + kMW);
-constexpr unsigned long long kWaitNs = 1000000000ull;   // a wait gives up after 1 s
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint32_t kWaitNs = 1000000000u;   // a wait gives up after 1 s
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // Decays below 2^-256 are zero in fp32 many times over: per-token log-decays
 // are clamped there, which keeps the block sums exact to 2^-10.
 constexpr float kMinLog = -256.f;
@@ -81,6 +85,15 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// 2^x - 1 for x in [-1, 0], to fp32: the exponential's series, x ln2 / 1! + ... (the
+// twelfth term is 1e-9 of the value; a call of expm1f costs the walk's tables registers).
+__device__ __forceinline__ float ex2m1(float x) {
+    x *= kLn2;
+    float y = 1.f;
+#pragma unroll
+    for (int i = 11; i > 1; --i) y = fmaf(x * (1.f / i), y, 1.f);
+    return x * y;
+}
 // One lane of a converged warp, in the form that lets the compiler keep MMA
 // operands in uniform registers: behind a plain `lane == 0` each MMA cost
 // 150-180 cycles to issue, 62 (its execution time at N = 128) behind this.
@@ -89,26 +102,23 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
     return e != 0;
 }
-// The slow part of a wait: until the phase completes, for at most kWaitNs (the
-// clock and the abort flag are read once in 64 polls).  Out of line: the roles
-// of a CTA run different code, and what is inlined at every wait pushes the
-// others out of the instruction cache.
-static __device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort_s,
-                                              unsigned int *err) {
-    const unsigned long long t0 = global_ns();
-    for (;;) {
-        if (mbar_wait(bar, parity, 64)) return true;
-        if (*abort_s) return false;
-        if (global_ns() - t0 >= kWaitNs) {
+__device__ __forceinline__ uint32_t global_ns_lo() {
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
+}
+// Wait for a phase, for at most kWaitNs; false when it, or another role's, gave up
+// (counted once, at the kernel's end).  Short, for it is inlined at every wait: the
+// roles of a CTA run different code that shares the instruction cache.
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t ph, volatile int *abort_s) {
+    if (mbar_try_wait(bar, ph & 1u)) return true;
+    const uint32_t t0 = global_ns_lo();
+    while (!mbar_try_wait(bar, ph & 1u))
+        if (*abort_s || global_ns_lo() - t0 >= kWaitNs) {
             *abort_s = 1;
-            atomicAdd(err, 1u);
             return false;
         }
-    }
-}
-// Bounded wait; false when it, or another role's, gave up.
-__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t ph, volatile int *abort_s, unsigned int *err) {
-    return mbar_try_wait(bar, ph & 1u) || wait_slow(bar, ph & 1u, abort_s, err);
+    return true;
 }
 // A wait gave up: the products issued by this thread end before shared memory and TMEM go.
 __device__ __forceinline__ void drain_products(uint64_t *bar) {
@@ -181,9 +191,29 @@ struct Table {
     float c[kTok];
     float w[kTok];      // d_j P(end, j)
     float pre[4];       // log2 decay from the chunk's start to the block's
-    float dec, pad[3];  // P(end, start)
+    float dec;          // P(end, start), or that less one where it is above 1/2 (keep):
+    float keep;         // rounded as a number near one it would be off by as much as the
+    float pad[2];       // state of a head that forgets slowly, once a chunk
 };
 __device__ __forceinline__ int cf_off(int b) { return 16 * b * (b - 1); }   // 0, 32, 96
+
+// Registers a thread of the walk's warp groups, out of the launch's: the state's
+// warps hold 128 values of it.
+constexpr int kRegsLaunch = 96;
+constexpr int kRegsState = 176, kRegsSupport = 56, kRegsWeights = 72, kRegsOutput = 88;
+static_assert(kRegsState + kRegsSupport + (kCW / 4) * kRegsWeights + (kMW / 4) * kRegsOutput <=
+                  kRegsLaunch * (kThreads / 128), "register shares");
+template <int N, bool kInc>
+__device__ __forceinline__ void set_registers() {
+    if (kInc) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// Wait for tmem_ld16; x is not read before it.
+__device__ __forceinline__ void tmem_wait_ld16(float (&x)[16]) {
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) asm volatile("" : "+f"(x[i]));
+}
 
 struct Params {
     gdn::ssm::Args a;
@@ -233,7 +263,7 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 {
     constexpr int W = DV * HB;
     using SM = Smem<DK, W>;
-    // TMEM columns: G / M, R / Y, the state, two buffers of three 16-column terms of weighted values
+    // TMEM columns: G / M, R / Y, dS (the start state at first), two buffers of three 16-column terms of weighted values
     constexpr uint32_t cG = 0, cY = 128, cS = 256, cW = 384;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t sbase = smem_u32(smem);
@@ -254,13 +284,14 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     uint64_t *y_free = bars + 12;      // Y read out
     uint64_t *y_staged = bars + 13;    // [2] output tile written (a barrier a slot: chunk c + 1 may be done before
                                        // the storing warp looks at chunk c's, chunk c + 2 not)
-    uint64_t *s_ready = bars + 15;     // state decayed in TMEM, its copy written
+    uint64_t *s_ready = bars + 15;     // the state's copy written
     uint64_t *wx_ready = bars + 16;    // [2] weighted values written
     uint64_t *wx_free = bars + 18;     // [2] ... and read
-    uint64_t *s_full = bars + 20;      // state updated
+    uint64_t *s_full = bars + 20;      // what a chunk adds to the state complete
     uint64_t *tab_full = bars + 21;    // [2] decay tables written
     uint64_t *tab_free = bars + 23;    // [2] ... and read
     uint64_t *drained = bars + 25;     // products complete, when a wait gave up
+    uint64_t *ds_free = bars + 26;     // what a chunk adds to the state has been read
     uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + SM::kCtl);
     volatile int *abort_s = reinterpret_cast<volatile int *>(smem + SM::kCtl + 4);
     Table *tabs = reinterpret_cast<Table *>(smem + SM::kTab);
@@ -299,10 +330,10 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             tma_load_4d(smem + SM::kQ + x * 16384, &tm_q, q_full, grp * DK + 64 * x, (c0 + c) * kTok, b, 0);
     };
     if (tid == 0) {
-        const uint8_t counts[26] = {1, 1, 1, 1, 1, 1, 1, 1, kCW, 1, kMW, 1, kMW, kMW, kMW, 4, 4, 4, 1, 1, 1, HB, HB,
-                                    4 + kCW + kMW, 4 + kCW + kMW, 1};
+        const uint8_t counts[27] = {1, 1, 1, 1, 1, 1, 1, 1, kCW, 1, kMW, 1, kMW, kMW, kMW, 4, 4, 4, 1, 1, 1, HB, HB,
+                                    4 + kCW + kMW, 4 + kCW + kMW, 1, 4};
 #pragma unroll
-        for (int i = 0; i < 26; ++i) mbar_init(bars + i, counts[i]);
+        for (int i = 0; i < 27; ++i) mbar_init(bars + i, counts[i]);
         fence_mbar_init();
         *abort_s = 0;
         // the first chunks' tiles, while the start state is gathered
@@ -376,11 +407,14 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     __syncthreads();
     tc_fence_after();
 
-    auto wait = [&](uint64_t *bar, uint32_t ph) { return wait_phase(bar, ph, abort_s, p.err); };
+    auto wait = [&](uint64_t *bar, uint32_t ph) { return wait_phase(bar, ph, abort_s); };
     auto partial = [&](int c) { return (c0 + c + 1) * kTok > n; };          // chunk with tokens behind the end
     // its rows behind the end are other sequences' memory only when n < T
     auto own_rows = [&](int c) { return partial(c) && n < p.a.T; };
 
+    if (warp >= 4 && warp < 8) {
+        set_registers<kRegsSupport, false>();
+    }
     if (warp == 4) {
         // ============================ loads and stores ==============================
         if (lane == 0) {
@@ -444,8 +478,8 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     mma_bf16(tmem + cG, adv(dQ, o), adv(dK, ks + o), idG, k > 0);
                 }
                 mma_commit(g_full);
-                if (!wait(s_ready, c)) break;
-                // S += dS, 32 tokens at a time
+                if (!wait(ds_free, c)) break;
+                // dS, 32 tokens at a time
                 bool ok = true;
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q, ++wph) {
@@ -453,6 +487,7 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     // the tensor cores busy (before it: 453 us on 4 x 16,384 x 32 x 128, so 440)
                     if (q == 1) {
                         if (c > 0 && !(ok = wait(y_free, c - 1))) break;
+                        if (!(ok = wait(s_ready, c))) break;
                         tc_fence_after();
 #pragma unroll
                         for (int k = 0; k < DK / 16; ++k)
@@ -464,11 +499,11 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     tc_fence_after();
                     const uint32_t wx = tmem + cW + (q & 1) * 48;
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        const uint64_t bk = adv(dKm, ks + (2 * q + s) * 2048);
+                    for (int t = 2; t >= 0; --t)      // the small terms first
 #pragma unroll
-                        for (int t = 0; t < 3; ++t) mma_bf16_ta(tmem + cS, wx + 16 * t + 8 * s, bk, idS, 1);
-                    }
+                        for (int s = 0; s < 2; ++s)
+                            mma_bf16_ta(tmem + cS, wx + 16 * t + 8 * s, adv(dKm, ks + (2 * q + s) * 2048), idS,
+                                        q + s + (2 - t) > 0);
                     mma_commit(&wx_free[q & 1]);
                 }
                 if (!ok) break;
@@ -549,13 +584,16 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 tb.pre[1] = sum[0];
                 tb.pre[2] = sum[0] + sum[1];
                 tb.pre[3] = sum[0] + sum[1] + sum[2];
-                tb.dec = ex2(post);
+                const bool keep = post > -1.f;
+                tb.keep = keep ? 1.f : 0.f;
+                tb.dec = keep ? ex2m1(post) : ex2(post);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&tab_full[c & 1]);
         }
     } else if (warp >= 8 + kCW) {
         // ============================ M and the output ==============================
+        set_registers<kRegsOutput, false>();
         constexpr int NG = kMW / 4;                  // warp groups
         const int u = (warp - 8 - kCW) >> 2;         // tokens 32 u .. of M (and every NG-th block), columns u NCOL ..
         const int row = quarter * 32 + lane;
@@ -684,6 +722,7 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         // This warp's 32 value columns are its 32 TMEM lanes: the values come out
         // of shared memory transposed (8 x 8 blocks), and the blocks of 8 tokens
         // are 16x128b pieces of the operand.
+        set_registers<kRegsWeights, false>();
         constexpr int NG = kCW / 4;
         const int u = (warp - 8) >> 2;               // blocks of 32 tokens u, u + NG, ..
         const int xcol = quarter * 32;
@@ -734,67 +773,81 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         }
     } else if (warp < 4) {
         // ============================ the state =====================================
+        // A thread's column of the state stays in its registers; TMEM holds what the
+        // chunk before adds to it (at first the start state).
+        set_registers<kRegsState, true>();
         const int v = quarter * 32 + lane;           // value column (TMEM lane)
         const bool live = v < W;
         const int hv = v / DV < HB ? v / DV : 0, vcol = v % DV;
         const size_t bh = (size_t)(b * p.a.H + h0 + hv);
         const uint32_t scol = tmem + lane_base + cS;
         const uint32_t sdst = SM::kS;
+        float2 S[DK / 2];
+        float dec = 0.f, keep = 0.f;                 // of the chunk before, as in its table
+#pragma unroll
+        for (int i = 0; i < DK / 2; ++i) S[i] = make_float2(0.f, 0.f);
+        // S <- P S + dS, 16 rows
+        auto add = [&](int k, const float *x) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)      // (no branch on keep: the compiler would copy the loop and spill S)
+                S[k / 2 + i] = fma2(keep, S[k / 2 + i], fma2(dec, S[k / 2 + i], make_float2(x[2 * i], x[2 * i + 1])));
+        };
         for (int c = 0; c < nch; ++c) {
-            // ---- the state after chunk c - 1: bf16 copy for R, decayed for chunk c
-            if (c > 0 && (!wait(s_full, c - 1) || !wait(r_done, c - 1))) break;
+            // ---- the state after chunk c - 1
+            if (c > 0 && !wait(s_full, c - 1)) break;
             tc_fence_after();
-            if (!wait(&tab_full[c & 1], c >> 1)) break;
-            const float dec = tabs[(c & 1) * 2 + hv].dec;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&tab_free[c & 1]);
-#pragma unroll 1
-            for (int k = 0; k < DK; k += 32) {
-                float x[2][16];
-                tmem_ld16(scol + k, x[0]);
-                tmem_ld16(scol + k + 16, x[1]);
-                tmem_wait_ld();
-                const uint32_t o = sdst + (k >> 6) * (W * 128) + swz128(v * 128 + (k & 63) * 2);
+            float x[2][16];
+            tmem_ld16(scol, x[0]);
+            tmem_wait_ld16(x[0]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float *y = x[e >> 1] + 8 * (e & 1);
-                    if (live)
-                        *reinterpret_cast<uint4 *>(smem + (o ^ (16 * e))) = make_uint4(
-                            pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        const float2 y = mul2(make_float2(x[e][i], x[e][i + 1]), make_float2(dec, dec));
-                        x[e][i] = y.x;
-                        x[e][i + 1] = y.y;
-                    }
-                    tmem_st16(scol + k + 16 * e, x[e]);
-                }
+            for (int k = 0; k < DK; k += 16) {
+                if (k + 16 < DK) tmem_ld16(scol + k + 16, x[((k >> 4) + 1) & 1]);
+                add(k, x[(k >> 4) & 1]);
+                if (k + 16 < DK) tmem_wait_ld16(x[((k >> 4) + 1) & 1]);
             }
-            tmem_wait_st();
-            fence_async_shared();
             tc_fence_before();
             __syncwarp();
+            if (lane == 0) mbar_arrive(ds_free);
+            // ---- its bf16 copy for R
+            if (c > 0 && !wait(r_done, c - 1)) break;
+            if (live)
+#pragma unroll
+                for (int k = 0; k < DK; k += 8) {
+                    const float2 *y = S + k / 2;
+                    *reinterpret_cast<uint4 *>(smem + sdst + (k >> 6) * (W * 128) + swz128(v * 128 + (k & 63) * 2)) =
+                        make_uint4(pack_bf16(y[0].x, y[0].y), pack_bf16(y[1].x, y[1].y), pack_bf16(y[2].x, y[2].y),
+                                   pack_bf16(y[3].x, y[3].y));
+                }
+            fence_async_shared();
+            __syncwarp();
             if (lane == 0) mbar_arrive(s_ready);
+            if (!wait(&tab_full[c & 1], c >> 1)) break;
+            dec = tabs[(c & 1) * 2 + hv].dec;
+            keep = tabs[(c & 1) * 2 + hv].keep;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tab_free[c & 1]);
         }
         if (last && p.a.state_out && nch > 0 && wait(s_full, nch - 1)) {
             tc_fence_after();
-#pragma unroll 1
+#pragma unroll
             for (int k = 0; k < DK; k += 16) {
                 float x[16];
                 tmem_ld16(scol + k, x);
-                tmem_wait_ld();
+                tmem_wait_ld16(x);
+                add(k, x);
                 if (live)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) p.a.state_out[(bh * DK + k + i) * DV + vcol] = x[i];
+                    for (int i = 0; i < 8; ++i) {
+                        p.a.state_out[(bh * DK + k + 2 * i) * DV + vcol] = S[k / 2 + i].x;
+                        p.a.state_out[(bh * DK + k + 2 * i + 1) * DV + vcol] = S[k / 2 + i].y;
+                    }
             }
         }
     }
 
     tc_fence_before();
     __syncthreads();
+    if (*abort_s && tid == 0) atomicAdd(p.err, 1u);
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
@@ -947,7 +1000,7 @@ tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     }
     __syncthreads();
     const int steps = max(1, max(steps_s[0], steps_s[HB - 1]));   // (the first tile is on its way)
-    auto wait = [&](uint64_t *bar, uint32_t ph) { return wait_phase(bar, ph, abort_s, p.err); };
+    auto wait = [&](uint64_t *bar, uint32_t ph) { return wait_phase(bar, ph, abort_s); };
     int issued = 1;                                               // loads (known to lane 0 of warp 16)
 
     if (warp == 16) {
@@ -1066,6 +1119,7 @@ tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     }
     tc_fence_before();
     __syncthreads();
+    if (*abort_s && tid == 0) atomicAdd(p.err, 1u);
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 

@@ -41,8 +41,9 @@ WALK = {
               _w("k_free[c & 1]", "c >> 1", "c + 2 < nch"), _l("k_full", "c + 2", "c + 2 < nch"),
               _w("y_staged[c & 1]", "c >> 1"), _l("x_full", "c + 2", "c + 2 < nch")],
     "mma": [_w("q_full", "c"), _w("k_full[c & 1]", "c >> 1"), _w("fixed", "0", "partial"),
-            _w("y_full", "c - 1", "c > 0"), _c("g_full"), _w("s_ready", "c"),
-            ("loop", "q", 4, [_w("y_free", "c - 1", "q == 1 and c > 0"), _c("r_done", "q == 1"),
+            _w("y_full", "c - 1", "c > 0"), _c("g_full"), _w("ds_free", "c"),
+            ("loop", "q", 4, [_w("y_free", "c - 1", "q == 1 and c > 0"), _w("s_ready", "c", "q == 1"),
+                              _c("r_done", "q == 1"),
                               _w("wx_ready[q & 1]", "wph >> 1"), _c("wx_free[q & 1]")]),
             _c("s_full"), _c("k_free[c & 1]"), _w("m_ready", "c"), _c("y_full")],
     "tables": [_w("tab_free[c & 1]", "(c >> 1) - 1", "c >= 2"), _a("tab_full[c & 1]")],
@@ -52,8 +53,8 @@ WALK = {
                 _a("fixed", "partial"), _w("fixed", "0", "partial"),
                 ("loop", "q", 4, [_w("wx_free[q & 1]", "use - 1", "use >= 1"), _a("wx_ready[q & 1]")]),
                 _a("tab_free[c & 1]")],
-    "state": [_w("s_full", "c - 1", "c > 0"), _w("r_done", "c - 1", "c > 0"), _w("tab_full[c & 1]", "c >> 1"),
-              _a("tab_free[c & 1]"), _a("s_ready")],
+    "state": [_w("s_full", "c - 1", "c > 0"), _a("ds_free"), _w("r_done", "c - 1", "c > 0"), _a("s_ready"),
+              _w("tab_full[c & 1]", "c >> 1"), _a("tab_free[c & 1]")],
 }
 # members of each role, as far as they tell apart: two stand for more
 WALK_ROLES = {"loads": 1, "mma": 1, "tables": 2, "output": 2, "weights": 2, "state": 2}
@@ -201,7 +202,8 @@ def _programs(model, roles, n, partial, consts):
 def _walk(n, partial, model=WALK):
     slots = dict(x_full=2, k_full=2)
     programs = _programs(model, WALK_ROLES, n, partial, dict(slots=slots))
-    two = {("m_ready", 0): 2, ("y_free", 0): 2, ("s_ready", 0): 2, ("fixed", 0): 2}
+    two = {("m_ready", 0): 2, ("y_free", 0): 2, ("s_ready", 0): 2, ("ds_free", 0): 2,
+           ("fixed", 0): 2}
     for s in (0, 1):
         two.update({("y_staged", s): 2, ("wx_ready", s): 2, ("tab_full", s): 2, ("tab_free", s): 6})
     started = [("k_full", 0), ("q_full", 0), ("x_full", 0)] + ([("k_full", 1), ("x_full", 1)] if n > 1 else [])
