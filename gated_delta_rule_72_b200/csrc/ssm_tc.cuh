@@ -855,6 +855,7 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 // Contributions of the segments to the states after them
 // ---------------------------------------------------------------------------
 constexpr int kTailStages = 3;
+constexpr int kTailBars = 17;              // barriers
 constexpr int kTailThreads = 32 * 22;      // 16 warps of weighted values, loads, MMA issue, 4 of weights
 constexpr int kMaxSegChunks = 256;         // longest segment (its blocks' decays are kept in shared memory)
 
@@ -864,7 +865,7 @@ struct TailSmem {
     static constexpr int kW = kTailStages * kStage;              // weights [2][2][128]
     static constexpr int kSum = kW + 4 * kTok * 4;               // log2 decay of each 32-token block [2][4 kMaxSegChunks]
     static constexpr int kBar = kSum + 8 * kMaxSegChunks * 4;
-    static constexpr int kCtl = kBar + 128;
+    static constexpr int kCtl = kBar + 8 * kTailBars;
     static constexpr int kBytes = kCtl + 32;
     static_assert(kBytes <= 232448, "shared memory budget");
 };
@@ -872,9 +873,9 @@ struct TailSmem {
 // grid (nseg - 1, B * nhb): segment g of a head block: tails[g] = the state
 // after it when it starts from zero, decs[g] = its log2 decay.  Segments without a successor do nothing.  The
 // chunks are taken from the last one back, until what is before has decayed
-// below kForgetLog; every product accumulates onto the state in TMEM, so that
-// the weighted values of one chunk are made while the chunk before is
-// multiplied.  A chunk costs about 1.6 us (three products over k, 1,500 cycles
+// below kForgetLog; each is summed from zero in TMEM and added in registers (as the
+// walk does, and for the same reason), behind the next one's weighted values, so
+// that these are made while a chunk is multiplied.  A chunk costs about 1.6 us (three products over k, 1,500 cycles
 // of them); 256 chunks of 12 head blocks in 11 segments take 42 us where some
 // heads never forget.
 template <int DK, int DV, int HB>
@@ -898,7 +899,9 @@ tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     uint64_t *w_free = bars + 8;       // [2] ... and read
     uint64_t *wx_ready = bars + 10;    // [2] weighted values written
     uint64_t *wx_free = bars + 12;     // [2] ... and read
-    uint64_t *done = bars + 14;
+    uint64_t *s_full = bars + 14;      // a chunk's sum complete
+    uint64_t *s_free = bars + 15;      // ... and read
+    uint64_t *drained = bars + 16;     // products complete, when a wait gave up
     uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + SM::kCtl);
     volatile int *abort_s = reinterpret_cast<volatile int *>(smem + SM::kCtl + 4);
     float *after_s = reinterpret_cast<float *>(smem + SM::kCtl + 8);     // [2]
@@ -932,7 +935,8 @@ tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     };
     if (tid == 0) {
 #pragma unroll
-        for (int i = 0; i < 15; ++i) mbar_init(bars + i, i >= 8 && i < 12 ? 16 : (i == 6 || i == 7 ? 4 : 1));
+        for (int i = 0; i < kTailBars; ++i)
+            mbar_init(bars + i, (i >= 8 && i < 12) || i == 15 ? 16 : (i == 6 || i == 7 ? 4 : 1));
         fence_mbar_init();
         *abort_s = 0;
         load(0);               // the last chunk counts whatever the decays are
@@ -1018,19 +1022,21 @@ tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             for (int i = 0; i < steps; ++i) {
                 const int st = i % kTailStages;
                 if (!wait(&full[st], i / kTailStages) || !wait(&wx_ready[i & 1], i >> 1)) break;
+                if (i > 0 && !wait(s_free, i - 1)) break;
                 tc_fence_after();
                 const uint64_t dK = sdesc_sw128_mn(sbase + st * SM::kStage + (W / 64) * 16384, 16384);
                 const uint32_t wx = tmem + cW + (i & 1) * 192;
 #pragma unroll
-                for (int s = 0; s < 8; ++s)
+                for (int t = 2; t >= 0; --t)      // the small terms first
 #pragma unroll
-                    for (int t = 0; t < 3; ++t)
+                    for (int s = 0; s < 8; ++s)
                         mma_bf16_ta(tmem + cS, wx + (s >> 1) * 48 + t * 16 + (s & 1) * 8, dK + s * 128, idS,
-                                    i + s + t > 0);
+                                    s + (2 - t) > 0);
                 mma_commit(&freed[st]);
                 mma_commit(&wx_free[i & 1]);
+                mma_commit(s_full);
             }
-            mma_commit(done);
+            if (*abort_s) drain_products(drained);
         }
         __syncwarp();
     } else if (warp >= 18) {
@@ -1068,54 +1074,74 @@ tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             if (lane == 0) mbar_arrive(&w_full[i & 1]);
         }
     } else {
-        // weighted values: token block warp / 4, value columns 32 quarter ..
+        // weighted values: token block warp / 4, value columns 32 quarter ..; behind
+        // them the sum of the chunk before, a quarter of d_k, onto the registers'
+        constexpr int NK = DK / 4;
         const int q = warp >> 2, xcol = quarter * 32;
-        for (int i = 0; i < steps; ++i) {
-            const int st = i % kTailStages;
-            if (!wait(&w_full[i & 1], i >> 1) || !wait(&full[st], i / kTailStages)) break;
-            float2 w[4] = {};
-            if (xcol < W) {
-                const float2 *wt =
-                    reinterpret_cast<const float2 *>(ws + ((i & 1) * 2 + xcol / DV) * kTok + q * 32) + (lane & 3);
+        float2 acc[NK / 2];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) w[k] = wt[4 * k];
+        for (int k = 0; k < NK / 2; ++k) acc[k] = make_float2(0.f, 0.f);
+        bool ok = true;
+        for (int i = 0; i <= steps; ++i) {
+            if (i < steps) {
+                const int st = i % kTailStages;
+                if (!(ok = wait(&w_full[i & 1], i >> 1) && wait(&full[st], i / kTailStages))) break;
+                float2 w[4] = {};
+                if (xcol < W) {
+                    const float2 *wt =
+                        reinterpret_cast<const float2 *>(ws + ((i & 1) * 2 + xcol / DV) * kTok + q * 32) + (lane & 3);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) w[k] = wt[4 * k];
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&w_free[i & 1]);
+                if (i >= 2 && !(ok = wait(&wx_free[i & 1], (i >> 1) - 1))) break;
+                tc_fence_after();
+                if (xcol < W)
+                    weigh_block(sbase + st * SM::kStage + (xcol >> 6) * 16384 +
+                                    swz128((q * 32 + lane) * 128 + (xcol & 63) * 2),
+                                tmem + ((uint32_t)(quarter * 32) << 16) + cW + (i & 1) * 192 + q * 48, w);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&wx_ready[i & 1]);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&w_free[i & 1]);
-            if (i >= 2 && !wait(&wx_free[i & 1], (i >> 1) - 1)) break;
-            tc_fence_after();
-            if (xcol < W)
-                weigh_block(sbase + st * SM::kStage + (xcol >> 6) * 16384 +
-                                swz128((q * 32 + lane) * 128 + (xcol & 63) * 2),
-                            tmem + ((uint32_t)(quarter * 32) << 16) + cW + (i & 1) * 192 + q * 48, w);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&wx_ready[i & 1]);
+            if (i > 0) {
+                if (!(ok = wait(s_full, i - 1))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < NK; k += 16) {
+                    float x[16];
+                    tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + cS + q * NK + k, x);
+                    tmem_wait_ld16(x);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        acc[k / 2 + j].x += x[2 * j];
+                        acc[k / 2 + j].y += x[2 * j + 1];
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_free);
+            }
         }
-        // ---- out: a quarter of d_k each
-        if (wait(done, 0)) {
-            tc_fence_after();
-            constexpr int NK = DK / 4;
-            const int u = warp >> 2, v = quarter * 32 + lane;
+        // ---- out
+        const int v = quarter * 32 + lane;
+        if (ok && v < W) {
             const int hv = v / DV < HB ? v / DV : 0, vcol = v % DV;
             const size_t bh = (size_t)(b * p.a.H + h0 + hv);
-            float *dst = tails + ((bh * (p.nseg - 1) + seg) * DK + u * NK) * DV + vcol;
-            float x[NK];
+            float *dst = tails + ((bh * (p.nseg - 1) + seg) * DK + q * NK) * DV + vcol;
 #pragma unroll
-            for (int k = 0; k < NK; k += 16)
-                tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + cS + u * NK + k, x + k);
-            tmem_wait_ld();
-            if (v < W)
-#pragma unroll
-                for (int i = 0; i < NK; ++i) dst[(size_t)i * DV] = x[i];
+            for (int k = 0; k < NK / 2; ++k) {
+                dst[(size_t)(2 * k) * DV] = acc[k].x;
+                dst[(size_t)(2 * k + 1) * DV] = acc[k].y;
+            }
         }
         if (tid < HB) decs[(size_t)(b * p.a.H + h0 + tid) * (p.nseg - 1) + seg] = after_s[tid];
     }
     __syncthreads();
     if (*abort_s && warp == 16 && lane == 0) {
-        // a wait gave up: copies and products end before shared memory and TMEM go
+        // a wait gave up: the copies land before shared memory goes
         for (int s = 0; s < kTailStages; ++s) mbar_drain(&full[s], (issued + kTailStages - 1 - s) / kTailStages);
-        mbar_drain(done, 1);
     }
     tc_fence_before();
     __syncthreads();

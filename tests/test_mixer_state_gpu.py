@@ -51,3 +51,11 @@ def check_long_walk(B, T, H, G, dk, dv):
                                            (4, 16384, 32, 8, 128, 128), (2, 300, 40, 1, 64, 128)])
 def test_state_of_whole_walks(B, T, H, G, dk, dv):
     check_long_walk(B, T, H, G, dk, dv)
+
+
+@pytest.mark.parametrize("B,T,H,G,dk,dv", [(1, 32760, 24, 1, 128, 64), (2, 1560, 16, 16, 128, 128),
+                                           (1, 20000, 1, 1, 64, 64), (1, 100000, 75, 75, 128, 128)])
+def test_state_of_segmented_walks(B, T, H, G, dk, dv):
+    """(Contributions of the segments are made of the same sums and join the walk with
+    one rounding each.)"""
+    check_long_walk(B, T, H, G, dk, dv)

@@ -62,10 +62,13 @@ WALK_SECTIONS = ["loads and stores", "MMA issue", "decay tables", "M and the out
 
 TAIL = {
     "loads": [_w("freed[i % kTailStages]", "i / kTailStages - 1", "i >= kTailStages"), _l("full", "i")],
-    "mma": [_w("full[st]", "i / kTailStages"), _w("wx_ready[i & 1]", "i >> 1"), _c("freed[st]"), _c("wx_free[i & 1]")],
+    "mma": [_w("full[st]", "i / kTailStages"), _w("wx_ready[i & 1]", "i >> 1"),
+            _w("s_free", "i - 1", "i > 0"), _c("freed[st]"), _c("wx_free[i & 1]"), _c("s_full")],
     "gates": [_w("w_free[i & 1]", "(i >> 1) - 1", "i >= 2"), _a("w_full[i & 1]")],
-    "weights": [_w("w_full[i & 1]", "i >> 1"), _w("full[st]", "i / kTailStages"), _a("w_free[i & 1]"),
-                _w("wx_free[i & 1]", "(i >> 1) - 1", "i >= 2"), _a("wx_ready[i & 1]")],
+    # (goes one step further than the others)
+    "weights": [_w("w_full[i & 1]", "i >> 1", "i < steps"), _w("full[st]", "i / kTailStages", "i < steps"),
+                _a("w_free[i & 1]", "i < steps"), _w("wx_free[i & 1]", "(i >> 1) - 1", "2 <= i < steps"),
+                _a("wx_ready[i & 1]", "i < steps"), _w("s_full", "i - 1", "i > 0"), _a("s_free", "i > 0")],
 }
 TAIL_ROLES = {"loads": 1, "mma": 1, "gates": 2, "weights": 2}
 
@@ -118,10 +121,9 @@ def test_walk_source_has_the_modelled_order():
 def test_tail_source_has_the_modelled_order():
     text = _kernel("tail_kernel")
     cuts = [text.index(s) for s in ("if (warp == 16)", "else if (warp == 17)", "else if (warp >= 18)",
-                                    "const int q = warp >> 2, xcol")] + [text.index("if (wait(done, 0))")]
+                                    "const int q = warp >> 2, xcol")] + [text.index("if (ok && v < W)")]
     for (role, ops), a, b in zip(TAIL.items(), cuts, cuts[1:]):
-        got = [op for op in _source_ops(text[a:b]) if op != ("commit", "done", None)]
-        assert got == _model_ops(ops), role
+        assert _source_ops(text[a:b]) == _model_ops(ops), role
 
 
 class _Run:
@@ -192,8 +194,8 @@ def _programs(model, roles, n, partial, consts):
     for role, count in roles.items():
         for i in range(count):
             ops = []
-            for c in range(n):
-                env = dict(c=c, i=c, nch=n, partial=partial and c == n - 1, kTailStages=3, st=c % 3)
+            for c in range(n + consts.get("further", {}).get(role, 0)):
+                env = dict(c=c, i=c, nch=n, steps=n, partial=partial and c == n - 1, kTailStages=3, st=c % 3)
                 ops += expand([o for o in model[role] if not (o[0] == "load" and o[1] == "full" and c == 0)], env)
             out[role, i] = ops
     return out
@@ -211,8 +213,8 @@ def _walk(n, partial, model=WALK):
 
 
 def _tail(n, model=TAIL):
-    programs = _programs(model, TAIL_ROLES, n, False, dict(slots=dict(full=3)))
-    two = {}
+    programs = _programs(model, TAIL_ROLES, n, False, dict(slots=dict(full=3), further=dict(weights=1)))
+    two = {("s_free", 0): 2}
     for s in (0, 1):
         two.update({("w_full", s): 2, ("w_free", s): 2, ("wx_ready", s): 2})
     return lambda: _Run(programs, two, [("full", 0)])
@@ -292,7 +294,8 @@ def test_the_way_out_waits_for_the_last_load_of_every_slot():
     walk, tail, cols = _drains(_kernel("walk_kernel")), _drains(_kernel("tail_kernel")), _drains(_cols_source())
     assert {b for b, _ in walk} == {"q_full", "k_full[s]", "x_full[s]"}
     assert "if (*abort_s) drain_products(drained);" in _kernel("walk_kernel")
-    assert {b for b, _ in tail} == {"full[s]", "done"} and {b for b, _ in cols} == {"full + i"}
+    assert "if (*abort_s) drain_products(drained);" in _kernel("tail_kernel")
+    assert {b for b, _ in tail} == {"full[s]"} and {b for b, _ in cols} == {"full + i"}
     for n in range(12):
         assert _uses(walk, "q_full", nq=n) == n
         for s in range(2):
