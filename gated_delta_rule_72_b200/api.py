@@ -255,6 +255,14 @@ def _cuda(t, name):
     return t.device, code
 
 
+def _on(device, fn, *args):
+    """fn(*args) with `device` current."""
+    if device.index == torch._C._cuda_getDevice():
+        return fn(*args)
+    with torch.cuda.device(device):
+        return fn(*args)
+
+
 def _run(name, device, fn, *args):
     """fn(*args, stream) with `device` current, on its current stream."""
     if device.index == torch._C._cuda_getDevice():
@@ -442,8 +450,17 @@ def rotary(q, k, pos, freqs, *, interleaved=False, scale=1.0, q_out=None, k_out=
     return q_out, k_out
 
 
-def ssm_workspace_size(B, T, H, G, dk, dv, dtype=torch.bfloat16) -> int:
-    return _lib.gdn_ssm_workspace_size(B, T, H, G, dk, dv, _DT[dtype])
+def ssm_workspace_size(B, T, H, G, dk, dv, dtype=torch.bfloat16, device=None) -> int:
+    """Bytes of workspace that ssm_scan needs for these sizes on `device` (a CUDA
+    device; the current one by default: the plan goes by its number of SMs)."""
+    args = (B, T, H, G, dk, dv, _DT[dtype])
+    if device is None:
+        return _lib.gdn_ssm_workspace_size(*args)
+    device = torch.device(device)
+    if device.type != "cuda":
+        raise ValueError("device must be a CUDA device, got %s" % device)
+    return _lib.gdn_ssm_workspace_size(*args) if device.index is None else \
+        _on(device, _lib.gdn_ssm_workspace_size, *args)
 
 
 def ssm_scan(q, k, v, dt, A, D=None, dt_bias=None, state=None, *, softplus=True, lengths=None, return_state=True,
@@ -500,7 +517,7 @@ def ssm_scan(q, k, v, dt, A, D=None, dt_bias=None, state=None, *, softplus=True,
     elif return_state:
         state_out = A.new_empty(sshape)
     lib = _lib.load()
-    nbytes = lib.gdn_ssm_workspace_size(B, T, H, G, dk, dv, code)
+    nbytes = _on(dev, lib.gdn_ssm_workspace_size, B, T, H, G, dk, dv, code)
     ws = None
     if nbytes:
         if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
