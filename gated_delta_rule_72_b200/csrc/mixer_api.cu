@@ -74,7 +74,7 @@ bool distinct(const View &v) {
 }
 
 // Two views may share memory: their spans overlap and they are not disjoint
-// columns of the same rows (or of the same batch entries).
+// columns of the same rows, batch entries or heads.
 bool clash(const View &x, const View &y, size_t es) {
     if (!overlap(x.p, x.all() * es, y.p, y.all() * es)) return false;
     const long long bytes = static_cast<const char *>(y.p) - static_cast<const char *>(x.p);
@@ -90,6 +90,10 @@ bool clash(const View &x, const View &y, size_t es) {
     if (x.B > 1 && x.bs == y.bs && apart(x.batch(), y.batch(), x.bs)) return false;
     if (x.T > 1 && x.ts == y.ts && x.ts > 0 && (x.B == 1 || (x.bs == y.bs && x.bs % x.ts == 0)) &&
         apart(x.row(), y.row(), x.ts))
+        return false;
+    auto period = [&](int n, size_t a, size_t b) { return n == 1 || (a == b && a % x.hs == 0); };
+    if (x.H > 1 && x.hs == y.hs && x.hs > 0 && period(x.T, x.ts, y.ts) && period(x.B, x.bs, y.bs) &&
+        apart((size_t)x.d, (size_t)y.d, x.hs))
         return false;
     return true;
 }
