@@ -348,9 +348,12 @@ def rotary_freqs(rot_dim, *, base=10000.0, scaling="none", factor=1.0, original_
     the factor on the rotated channels (1 but for "yarn").
       theta_j = base^(-2j/rot_dim)
       scaling "linear": theta / factor;  "ntk": base * factor^(rot_dim/(rot_dim-2));
-      "yarn" (Peng et al. 2023): pairs that turn more than beta_fast times over
-      original_len positions keep theta, those below beta_slow take
-      theta / factor, a ramp between; scale = 0.1 ln(factor) + 1.
+      "yarn" (Peng et al. 2023), factor >= 1: pairs that turn more than beta_fast
+      times over original_len positions keep theta, those below beta_slow take
+      theta / factor, between them the weight of theta rises linearly with the
+      turns, as the paper has it (models trained with a ramp over the pairs'
+      numbers differ in the pairs between and need a table of their own);
+      scale = 0.1 ln(factor) + 1.
       axes: channels per position axis (even, summing to rot_dim), for instance
       (44, 42, 42) for frame, row and column; axis a of n_a channels has
       theta_j = base^(-2j/n_a)."""
@@ -376,6 +379,8 @@ def rotary_freqs(rot_dim, *, base=10000.0, scaling="none", factor=1.0, original_
             if scaling == "linear":
                 th /= factor
             elif scaling == "yarn":
+                if not factor >= 1:
+                    raise ValueError("yarn scaling lengthens a context: factor must be at least 1, got %r" % (factor,))
                 if original_len is None or not original_len > 0 or not beta_fast > beta_slow:
                     raise ValueError("yarn scaling needs original_len > 0 and beta_fast > beta_slow")
                 ramp = (original_len * th / (2 * math.pi) - beta_slow) / (beta_fast - beta_slow)
