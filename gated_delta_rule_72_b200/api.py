@@ -287,12 +287,13 @@ def short_conv(x, w, bias=None, state=None, *, silu=True, lengths=None, return_s
     """Short causal convolution over time, one filter per channel:
     y[b,t,c] = act(bias[c] + sum_j w[c,j] x[b,t-(K-1)+j,c]), act = silu or none.
 
-    x: [B,T,C] (fp32 or bf16, any batch and token stride); w: [C,K] fp32, K in
-    2..4; bias: [C] fp32 or None; state: [B,K-1,C] of x's dtype, the inputs
-    before token 0, oldest first (None = zero); lengths: [B] int32, tokens of
-    each sequence of a padded batch.  Returns (y, last K-1 inputs) (the state
-    None if not asked).  A new y is zero behind a sequence's end, a given
-    `out` keeps what it held there."""
+    x: [B,T,C] (fp32 or bf16, any batch and token stride of at least C); w:
+    [C,K] fp32, K in 2..4; bias: [C] fp32 or None; state: [B,K-1,C] of x's
+    dtype, the inputs before token 0, oldest first (None = zero); lengths: [B]
+    int32, tokens of each sequence of a padded batch.  Returns (y, last K-1
+    inputs) (the state None if not asked).  A new y is zero behind a sequence's
+    end (a fill of the whole of it before the call), a given `out` keeps what
+    it held there."""
     dev, dtype = x.device, x.dtype
     code = _DT.get(dtype)
     if x.dim() != 3 or w.dim() != 2:
@@ -475,12 +476,18 @@ def ssm_scan(q, k, v, dt, A, D=None, dt_bias=None, state=None, *, softplus=True,
     o_t = S_t^T q_t + D v_t.
 
     q, k: [B,T,G,dk] (G groups, each shared by H/G heads), v: [B,T,H,dv], fp32
-    or bf16, any batch and token stride (multiples of 16 bytes); dt: [B,T,H]
-    fp32 or q's dtype, any batch and token stride; A (<= 0), D, dt_bias: [H]
-    fp32; state: [B,H,dk,dv] fp32 (None = zero); lengths: [B] int32, tokens of
-    each sequence of a padded batch.  Returns (o, final state) (the state None
-    if not asked), o in q's dtype.  A new o is zero behind a sequence's end, a
-    given `out` keeps what it held there."""
+    or bf16, any batch and token stride of at least a row (multiples of 16
+    bytes); dt: [B,T,H] fp32 or q's dtype, any batch and token stride of at
+    least H; A (<= 0, -inf too), D, dt_bias: [H] fp32; state: [B,H,dk,dv] fp32
+    (None = zero); lengths: [B] int32, tokens of each sequence of a padded
+    batch.  Returns (o, final state) (the state None if not asked), o in q's
+    dtype.  A new o is zero behind a sequence's end (a fill of the whole of it
+    before the scan), a given `out` keeps what it held there.
+
+    Calls of more than 32 tokens go in chunks (128 tokens of bf16, 64 of fp32,
+    where that is faster): there an infinite or NaN value in v reaches earlier
+    outputs of its head and chunk too, in single tokens and short calls later
+    ones only."""
     dev, dtype = q.device, q.dtype
     code = _DT.get(dtype)
     if q.dim() != 4 or v.dim() != 4 or dt.dim() != 3:

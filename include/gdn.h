@@ -290,8 +290,10 @@ GDN_API gdn_status gdn_readout_gate(const void *o, gdn_dtype o_dt, const void *z
  * convolution, rotary positions) and the scan without the erase term (a
  * selective state space scan).  Unlike the scans above their inputs may be
  * views: batch, token (and head) strides are in ELEMENTS, the last dimension
- * is contiguous.  Outputs are contiguous unless strides are given.  The
- * stride of a dimension of one entry is not read.
+ * is contiguous.  Strides are at least a row's width, in any order (rows that
+ * are shared by a stride of 0 are taken by gdn_rotary's inputs only).  Outputs
+ * are contiguous unless strides are given.  The stride of a dimension of one
+ * entry is not read.
  * lengths (device, [B] int32, or NULL) gives the tokens of each sequence of a
  * padded batch, clamped to 0..T: inputs behind a sequence are not used (any
  * value, NaN too), outputs behind it are left as they were, and the final
@@ -364,12 +366,15 @@ GDN_API gdn_status gdn_rotary(const void *q, size_t q_batch_stride, size_t q_tok
  *   Paths    bf16: calls of more than 32 tokens run on the tensor cores in
  *            chunks of 128 tokens (the masked scores and the operand copy of
  *            the state are rounded to bf16 once: about 1.2 times the rounding
- *            of o itself; the state keeps fp32 accuracy), long ones in
- *            segments that run in parallel, which drops contributions that
- *            have decayed below 2^-100.  fp32: in chunks of 64 tokens or token
- *            by token, whichever the sizes make faster.  Within a chunk a
- *            token whose inputs are infinite or NaN reaches the chunk's
- *            earlier outputs too.
+ *            of o itself; the state stays within 1e-6 of its norm, however
+ *            long the call), long ones in segments that run in parallel, which
+ *            drops contributions that have decayed below 2^-100 (infinite and
+ *            NaN ones too).  fp32: in chunks of 64 tokens or token
+ *            by token, whichever the sizes make faster.  Within a chunk an
+ *            infinite or NaN v reaches its head's earlier outputs too (it meets
+ *            the zeros of the masked scores); q, k and dt do not, nor does
+ *            anything reach earlier chunks, other heads or other sequences.
+ *            Token by token no earlier output is reached at all.
  *   workspace  gdn_ssm_workspace_size(...) bytes for the same sizes on the
  *            same device, 256-byte aligned (NULL when that is 0); calls that
  *            may overlap in time need one each.
