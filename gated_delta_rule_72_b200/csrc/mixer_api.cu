@@ -73,29 +73,57 @@ bool distinct(const View &v) {
     return true;
 }
 
-// Two views may share memory: their spans overlap and they are not disjoint
-// columns of the same rows, batch entries or heads.
+// A dimension in which two views step alike, and what the smaller ones span in each.
+struct Step {
+    long long nx, ny, stride, ext_x, ext_y;
+};
+// Blocks of two views, `off` elements apart, share an element: for each
+// difference of the two indices in the largest dimension at which what lies below may
+// meet, look there.
+bool blocks_meet(const Step *st, int n, long long off, long long ext_x, long long ext_y) {
+    if (off >= ext_x || off + ext_y <= 0) return false;
+    if (n == 0) return true;
+    const long long p = st->stride;
+    long long lo = (-off - st->ext_y) / p - 1, hi = (st->ext_x - off) / p + 1;    // (one more on either side)
+    if (lo < -(st->nx - 1)) lo = -(st->nx - 1);
+    if (hi > st->ny - 1) hi = st->ny - 1;
+    if (hi - lo > 8) return true;                 // views that overlap themselves: not told apart
+    for (long long m = lo; m <= hi; ++m)
+        if (blocks_meet(st + 1, n - 1, off + m * p, st->ext_x, st->ext_y)) return true;
+    return false;
+}
+
+// Two views may share memory.  Exact where their strides are the same (one
+// tensor's heads, columns or rows, in any order of the dimensions); a dimension in
+// which the strides differ counts as one solid block.
 bool clash(const View &x, const View &y, size_t es) {
     if (!overlap(x.p, x.all() * es, y.p, y.all() * es)) return false;
     const long long bytes = static_cast<const char *>(y.p) - static_cast<const char *>(x.p);
     if (bytes % (long long)es) return true;
-    const long long off = bytes / (long long)es;
-    // [0, nx) and [off, off + ny) are disjoint in every period
-    auto apart = [off](size_t nx, size_t ny, size_t period) {
-        const long long p = (long long)period;
-        if (off <= -p || off >= p) return false;
-        const long long o = off < 0 ? off + p : off;
-        return o >= (long long)nx && o + (long long)ny <= p;
-    };
-    if (x.B > 1 && x.bs == y.bs && apart(x.batch(), y.batch(), x.bs)) return false;
-    if (x.T > 1 && x.ts == y.ts && x.ts > 0 && (x.B == 1 || (x.bs == y.bs && x.bs % x.ts == 0)) &&
-        apart(x.row(), y.row(), x.ts))
-        return false;
-    auto period = [&](int n, size_t a, size_t b) { return n == 1 || (a == b && a % x.hs == 0); };
-    if (x.H > 1 && x.hs == y.hs && x.hs > 0 && period(x.T, x.ts, y.ts) && period(x.B, x.bs, y.bs) &&
-        apart((size_t)x.d, (size_t)y.d, x.hs))
-        return false;
-    return true;
+    const int nx[3] = {x.B, x.T, x.H}, ny[3] = {y.B, y.T, y.H};
+    const size_t sx[3] = {x.bs, x.ts, x.hs}, sy[3] = {y.bs, y.ts, y.hs};
+    Step st[3];
+    int n = 0;
+    long long ext_x = x.d, ext_y = y.d;
+    for (int i = 0; i < 3; ++i) {
+        const long long s = (long long)(nx[i] > 1 ? sx[i] : sy[i]);
+        if (s == 0 || (nx[i] == 1 && ny[i] == 1)) continue;
+        if (nx[i] > 1 && ny[i] > 1 && sx[i] != sy[i]) {
+            ext_x += (nx[i] - 1) * (long long)sx[i];
+            ext_y += (ny[i] - 1) * (long long)sy[i];
+            continue;
+        }
+        int at = n++;
+        for (; at > 0 && st[at - 1].stride < s; --at) st[at] = st[at - 1];
+        st[at] = {nx[i], ny[i], s, 0, 0};
+    }
+    for (int i = n - 1; i >= 0; --i) {
+        st[i].ext_x = ext_x;
+        st[i].ext_y = ext_y;
+        ext_x += (st[i].nx - 1) * st[i].stride;
+        ext_y += (st[i].ny - 1) * st[i].stride;
+    }
+    return blocks_meet(st, n, bytes / (long long)es, ext_x, ext_y);
 }
 
 gdn_status launch_status() { return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }
