@@ -290,14 +290,15 @@ gdn_status token_dims(const Scan &c) {
 // Calls of at most this many tokens run token by token.
 constexpr int kTokenCall = 32;
 // Fewest chunks of a walk that is cut, down to segments of one chunk: with them
-// the contributions' launch takes about 5 us and a chunk of the walk 3.3 (16 heads of
-// 128 x 128: 3 chunks 17.1 us whole, 18.0 cut; 4 chunks 20.3 and 18.4; 13
-// chunks 27.9 in segments of 3, 25.4 of 2).
+// the contributions' launch takes about 5 us and a chunk of the walk 3.0 (16 heads of
+// 128 x 128: 3 chunks 16.9 us whole, 20.2 cut; 4 chunks 18.8 and 18.1, where a
+// state is updated in place 19.8 and 20.8; 6 chunks 24.7 and 20.0, in place 25.8
+// and 22.2; 13 chunks 30.0 in segments of 3, 26.9 of 2).
 constexpr int kMinSegmented = 4;
 // A segment starts from the sum of the contributions before it (0.6 us each
 // where nothing has been forgotten), so more segments shorten the walk up to about
-// sqrt(12 chunks) of them: 18,944 tokens of one head that never forgets 46 us in
-// 37 segments of 4 chunks, 89 in 148 of one.
+// sqrt(12 chunks) of them: 18,944 tokens of one head that never forgets 49 us in
+// 37 segments of 4 chunks, 92 in 148 of one.
 constexpr int kSegSquare = 12;
 
 bool use_tc(int T, gdn_dtype t) { return t == GDN_BF16 && T > kTokenCall; }
@@ -311,8 +312,8 @@ size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // the walk takes 0.21 us a token at d_k = 128 (0.18 at 64) while every warp has
 // a scheduler of its own (4 an SM), and 0.23 of that more for each further warp
 // there; the chunks take 30 us (three launches) and 0.16 us for every block of 64
-// tokens x 128 x 64, 0.19 at d_k = 64 (2,048 tokens: 24 heads of 128 x 64 125 us
-// against 436; 384 heads of 64 x 64 1,130 us against 720).
+// tokens x 128 x 64, 0.19 at d_k = 64 (2,048 tokens: 24 heads of 128 x 64 110 us
+// against 436; 384 heads of 64 x 64 1,130 us against 717).
 bool use_chunks(int B, int T, int H, int dk, int dv, gdn_dtype t) {
     if (t != GDN_F32 || T <= kTokenCall) return false;
     const double warps = (double)B * H * dv / 8, per = warps / (4.0 * gdn::device_sm_count());
@@ -366,7 +367,12 @@ gdn_status chunk_dims(const Scan &c, const ChunkPlan &pl, void *ws) {
 }
 
 // Head blocks (128 value columns: two heads of 64 that share a group, else one
-// head) and the segments of their walks: as many as leave one wave of CTAs.
+// head) and the segments of their walks, the same number for each: as many as
+// leave one wave of CTAs where there are fewer head blocks than SMs, else one.  So
+// SMs stand idle where the SMs are no multiple of the head blocks: 16,384 tokens of
+// heads of 128 x 128, 0.19 ns a token and head of 148 or 296 heads, 0.21 of 128,
+// 0.33 of 76 (one walk a head on half of the GPU) and 0.35 of 149 (a second wave
+// of one).
 struct TcPlan {
     int hb, nhb, nC, nseg, L;
     size_t tails, decs, init, bytes;   // workspace offsets and size

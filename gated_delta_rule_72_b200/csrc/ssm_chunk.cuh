@@ -16,7 +16,7 @@
 // shared-memory reads that feed them (a 16-byte read of a warp takes four cycles
 // even where all its lanes want the same) and, with few chunks, by the chain of
 // loads and barriers of one block: 5 sequences of up to 777 tokens, 6 heads of
-// 64 x 64, 28 us; 2,048 tokens of 24 heads of 128 x 64 123 us.
+// 64 x 64, 28 us; 2,048 tokens of 24 heads of 128 x 64 110 us.
 #pragma once
 
 #include "packed.cuh"

@@ -35,10 +35,11 @@
 // (1,490 cycles of an SM's share at 1.9 GHz), keeps the tensor cores busy for
 // about 3,100 cycles (dS, three terms, half of it) and takes 5,600 to 6,600: the products, the
 // warps between them and the tiles' latency wait for one another in turn.
-// 4 x 16,384 tokens of 32 heads of 128 x 128 take 438 us, 3.1 TB/s (without
-// products 350, without the warps' arithmetic 336, without either 275; with v
-// loaded a chunk earlier, into a slot still in use, 426).
-// 128-token chunks of 128 columns are the largest whose G/M, R/Y, S and
+// 4 x 16,384 tokens of 32 heads of 128 x 128 take 437 us at 1,965 MHz, 3.1 TB/s, and
+// 511 us call upon call, where the power limit (1,000 W) holds the clock at 1,620.
+// Left out in turn, with the state still in TMEM (438 us): the products 350, the
+// warps' arithmetic 336, both 275; v loaded a chunk earlier, into a slot still in use, 426.
+// 128-token chunks of 128 columns are the largest whose G/M, R/Y, dS and
 // weighted values fit TMEM's 512 columns; sharing G between two heads of 64
 // halves its cost and the q, k traffic.
 //
@@ -49,8 +50,9 @@
 //
 // Warps: 0-3 keep the state, 4 loads and stores (TMA), 5 issues every MMA, 6 and 7
 // make the decay tables, 8-11 the weighted values, 12-19 M and the output.
-// The state's warps come first because the next chunk waits for them (last,
-// with 16 warps for M: 519 us).
+// The state's warps come first because the next chunk waits for them, and release
+// what they have read of dS before they write the state's copy (together 515
+// us for what took 502).
 #pragma once
 
 #include "packed.cuh"
@@ -875,9 +877,11 @@ struct TailSmem {
 // chunks are taken from the last one back, until what is before has decayed
 // below kForgetLog; each is summed from zero in TMEM and added in registers (as the
 // walk does, and for the same reason), behind the next one's weighted values, so
-// that these are made while a chunk is multiplied.  A chunk costs about 1.6 us (three products over k, 1,500 cycles
-// of them); 256 chunks of 12 head blocks in 11 segments take 42 us where some
-// heads never forget.
+// that these are made while a chunk is multiplied (between their halves: 152 us for
+// what takes 146 of 32,760 tokens of 24 heads of 128 x 64; all chunks in one
+// accumulator, with its cuts: 142).  A chunk costs about 1.9 us (three products over k,
+// 1,500 cycles of them); 256 chunks of 12 head blocks in 11 segments take 47 us, 49
+// where no head forgets.
 template <int DK, int DV, int HB>
 __global__ void __launch_bounds__(kTailThreads, 1)
 tail_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Params p,
