@@ -15,9 +15,9 @@
 // Bound by the latency of a warp's own chain while each has a scheduler to itself
 // (0.21 us a token at d_k = 128: 512 tokens of 16 heads of 128 x 128 114 us), then
 // by issue, about 24 + 0.4 d_k instructions a token and warp.  fp32 throughout,
-// sums of d_k / 16 terms per lane; decays are the nearest fp32 (as the part lost, which
-// is exact for slow heads too, each state element costs an operation more: 202 -> 229
-// us for 128 sequences of 24 tokens, 32 heads of 128 x 64).
+// sums of d_k / 16 terms per lane; decays are the nearest fp32 (with what they leave,
+// as for single tokens, each state element costs an operation more: 202 -> 229 us
+// for 128 sequences of 24 tokens, 32 heads of 128 x 64).
 #pragma once
 
 #include "packed.cuh"

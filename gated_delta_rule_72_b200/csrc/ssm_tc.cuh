@@ -193,9 +193,8 @@ struct Table {
     float c[kTok];
     float w[kTok];      // d_j P(end, j)
     float pre[4];       // log2 decay from the chunk's start to the block's
-    float dec;          // P(end, start), or that less one where it is above 1/2 (keep):
-    float keep;         // rounded as a number near one it would be off by as much as the
-    float pad[2];       // state of a head that forgets slowly, once a chunk
+    gdn::ssm::Decay dec;   // P(end, start)
+    float pad[2];
 };
 __device__ __forceinline__ int cf_off(int b) { return 16 * b * (b - 1); }   // 0, 32, 96
 
@@ -586,9 +585,8 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 tb.pre[1] = sum[0];
                 tb.pre[2] = sum[0] + sum[1];
                 tb.pre[3] = sum[0] + sum[1] + sum[2];
-                const bool keep = post > -1.f;
-                tb.keep = keep ? 1.f : 0.f;
-                tb.dec = keep ? ex2m1(post) : ex2(post);
+                tb.dec = post > -1.f ? gdn::ssm::decay_near_one(ex2m1(post))
+                                     : gdn::ssm::Decay{ex2(post), gdn::ssm::kTiny};
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&tab_full[c & 1]);
@@ -785,14 +783,15 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         const uint32_t scol = tmem + lane_base + cS;
         const uint32_t sdst = SM::kS;
         float2 S[DK / 2];
-        float dec = 0.f, keep = 0.f;                 // of the chunk before, as in its table
+        gdn::ssm::Decay dec{0.f, 0.f};               // of the chunk before
 #pragma unroll
         for (int i = 0; i < DK / 2; ++i) S[i] = make_float2(0.f, 0.f);
         // S <- P S + dS, 16 rows
         auto add = [&](int k, const float *x) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)      // (no branch on keep: the compiler would copy the loop and spill S)
-                S[k / 2 + i] = fma2(keep, S[k / 2 + i], fma2(dec, S[k / 2 + i], make_float2(x[2 * i], x[2 * i + 1])));
+            for (int i = 0; i < 8; ++i)
+                S[k / 2 + i] = fma2(dec.a, S[k / 2 + i],
+                                    fma2(dec.e, S[k / 2 + i], make_float2(x[2 * i], x[2 * i + 1])));
         };
         for (int c = 0; c < nch; ++c) {
             // ---- the state after chunk c - 1
@@ -825,7 +824,6 @@ walk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if (lane == 0) mbar_arrive(s_ready);
             if (!wait(&tab_full[c & 1], c >> 1)) break;
             dec = tabs[(c & 1) * 2 + hv].dec;
-            keep = tabs[(c & 1) * 2 + hv].keep;
             __syncwarp();
             if (lane == 0) mbar_arrive(&tab_free[c & 1]);
         }

@@ -47,17 +47,28 @@ __device__ __forceinline__ float decay(float d, float A) {
     const float x = log_decay(d, A);
     return x > -0.5f ? 1.f + expm1f(x) : expf(x);
 }
-// The same as S <- keep S + (m S + d k v^T): m is what is lost, a - 1, where a is above
-// 1/2 (keep 1), else a itself (keep 0).  Near one even the nearest a is off by up
-// to 2^-25, as much as a slow head forgets: 2e-5 of the state's norm behind 3,000
-// tokens, 6e-5 with expf, 1.4e-6 in this form.  It costs a multiply-add for each element of
-// the state, which is free where the state comes from memory for every token.
+// A decay as a + e, a the fp32 below it: S <- a S + (e S + d k v^T).  Near one even the
+// nearest fp32 is off by up to 2^-25, as much as a slow head forgets: 2e-5 of the
+// state's norm behind 3,000 tokens, 6e-5 with expf, 1.4e-6 in this form.  It costs a
+// multiply-add for each element of the state, which is free where the state comes
+// from memory for every token.  e stays above zero: zero times an infinite element
+// would be NaN.
 struct Decay {
-    float m, keep;
+    float a, e;
 };
+constexpr float kTiny = 1e-30f;
+// From the decay less one, in [-1/2, 0].
+__device__ __forceinline__ Decay decay_near_one(float m) {
+    float a = 1.f + m, e = (1.f - a) + m;
+    if (e < 0.f) {
+        a -= 0x1p-24f;
+        e += 0x1p-24f;
+    }
+    return {a, fmaxf(e, kTiny)};
+}
 __device__ __forceinline__ Decay split_decay(float d, float A) {
     const float x = log_decay(d, A);
-    return x > -0.6931471805599453f ? Decay{expm1f(x), 1.f} : Decay{expf(x), 0.f};
+    return x > -0.6931471805599453f ? decay_near_one(expm1f(x)) : Decay{expf(x), kTiny};
 }
 
 constexpr int kTokThreads = 128;
@@ -103,10 +114,10 @@ token_kernel(const Args a)
 #pragma unroll
         for (int m = 0; m < RPT; ++m) {
             const float kr = ks[rg + RG * m], qr = qs[rg + RG * m];
-            S[m].x = fmaf(al.keep, S[m].x, fmaf(al.m, S[m].x, kr * u.x));
-            S[m].y = fmaf(al.keep, S[m].y, fmaf(al.m, S[m].y, kr * u.y));
-            S[m].z = fmaf(al.keep, S[m].z, fmaf(al.m, S[m].z, kr * u.z));
-            S[m].w = fmaf(al.keep, S[m].w, fmaf(al.m, S[m].w, kr * u.w));
+            S[m].x = fmaf(al.a, S[m].x, fmaf(al.e, S[m].x, kr * u.x));
+            S[m].y = fmaf(al.a, S[m].y, fmaf(al.e, S[m].y, kr * u.y));
+            S[m].z = fmaf(al.a, S[m].z, fmaf(al.e, S[m].z, kr * u.z));
+            S[m].w = fmaf(al.a, S[m].w, fmaf(al.e, S[m].w, kr * u.w));
             y.x = fmaf(qr, S[m].x, y.x);
             y.y = fmaf(qr, S[m].y, y.y);
             y.z = fmaf(qr, S[m].z, y.z);

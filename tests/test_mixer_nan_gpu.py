@@ -43,3 +43,41 @@ def test_convolution_with_a_value_that_is_not_finite(dtype):
     reached = torch.zeros_like(y, dtype=torch.bool)
     reached[1, 40:44, 5] = True
     assert torch.isnan(y2[reached]).all() and torch.equal(y[~reached], y2[~reached]) and torch.equal(last, last2)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T", [1, 4])
+@pytest.mark.parametrize("a", [-0.1, -3.0])
+def test_infinite_state_element_of_a_step(dtype, T, a):
+    """An infinite element stays what it is, the others do not learn of it, however
+    much the token forgets."""
+    c = _ssm_case(2, T, 2, 1, 64, 64, dtype, 4)
+    c = {n: t.clone() for n, t in c.items()}
+    c["A"].fill_(a)
+    c["dt"] = torch.ones(2, T, 2, device="cuda")
+    c["dt_bias"] = None
+    _, s = gdn.ssm_scan(**c, softplus=False)
+    c["state"][1, 0, 3, 5] = float("inf")
+    _, s2 = gdn.ssm_scan(**c, softplus=False)
+    other = torch.ones_like(s, dtype=torch.bool)
+    other[1, 0, 3, 5] = False
+    assert torch.equal(s[other], s2[other]) and s2[1, 0, 3, 5] == float("inf")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T", [300, 1000])
+def test_infinite_state_element_of_a_prompt(dtype, T):
+    c = _ssm_case(2, T, 2, 1, 64, 64, dtype, 5)
+    c = {n: t.clone() for n, t in c.items()}
+    c["A"].fill_(-0.01)
+    c["dt"] = torch.ones(2, T, 2, device="cuda")
+    c["dt_bias"] = None
+    o, s = gdn.ssm_scan(**c, softplus=False)
+    c["state"][1, 0, 3, 5] = float("inf")
+    o2, s2 = gdn.ssm_scan(**c, softplus=False)
+    other = torch.ones_like(s, dtype=torch.bool)
+    other[1, 0, 3, 5] = False
+    assert torch.equal(s[other], s2[other]) and s2[1, 0, 3, 5] == float("inf")
+    column = torch.ones_like(o, dtype=torch.bool)
+    column[1, :, 0, 5] = False
+    assert torch.equal(o[column], o2[column])
