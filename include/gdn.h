@@ -366,7 +366,7 @@ GDN_API gdn_status gdn_rotary(const void *q, size_t q_batch_stride, size_t q_tok
  *   Paths    bf16: calls of more than 32 tokens run on the tensor cores in
  *            chunks of 128 tokens (the masked scores and the operand copy of
  *            the state are rounded to bf16 once: about 1.2 times the rounding
- *            of o itself; the state stays within 1e-6 of its norm, however
+ *            of o itself; the state stays within 2e-6 of its norm, however
  *            long the call), long ones in segments that run in parallel, which
  *            drops contributions that have decayed below 2^-100 (infinite and
  *            NaN ones too).  fp32: in chunks of 64 tokens or token
